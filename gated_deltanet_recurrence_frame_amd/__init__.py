@@ -7,4 +7,4 @@ Importing the package does not load the library; the first binding call does,
 and it raises if the library is missing.
 """
 
-__all__ = ["binding", "inputs"]
+__all__ = ["binding", "block", "inputs"]

@@ -1,0 +1,511 @@
+"""Thin ctypes binding over the block's operators (include/gdn_block.h):
+queries and keys normalised and rotated by position (``QkPlan``,
+``qk_forward``, ``qk_backward``), 8-bit checkpoints of activation rows
+(``pack8``, ``unpack8``, ``Checkpoint``) and the gated linear recurrence
+(``LrecPlan``, ``lrec_forward``, ``lrec_step``, ``lrec_backward``).
+
+As in ``binding``: argument marshalling only, every tensor checked for device,
+dtype, shape and layout before the C entry point is called, everything runs
+in the HIP kernels of libgdn.so on torch's current stream of the tensors'
+device.  A plan holds outputs and workspace for repeated calls on one shape;
+its outputs are overwritten by its next call.  Inputs that come out of a
+projection may be slices of it: their last dimensions are contiguous, the
+batches and tokens at any stride.
+"""
+
+import collections
+import ctypes
+import os
+
+import torch
+
+from . import binding
+from .binding import (GDN_BF16, GDN_FP32, GDN_OP_BACKWARD, GDN_OP_FORWARD, _check, _empty, _io_of,
+                      _need, _p)
+
+HEADER = os.path.join(os.path.dirname(binding.HEADER), "gdn_block.h")
+GDN_LREC_COMPLEMENT = 4
+NORMS = {"none": 0, "l2": 1, "rms": 2}
+PAIRINGS = {"halves": 0, "adjacent": 1}
+DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+# values float8_e4m3fn [B, L, H, D] (in units of the row's scale), scale uint8
+# [B, L, H]: a row is values * 2 ** (scale - 127)
+Checkpoint = collections.namedtuple("Checkpoint", ["values", "scale"])
+
+_VP = ctypes.c_void_p
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+_Pair = _I64 * 2
+
+
+class GdnCheckpoint(ctypes.Structure):
+    _fields_ = [("values", _VP), ("scale", _VP)]
+
+
+class GdnPack8Problem(ctypes.Structure):
+    _fields_ = [("B", _I32), ("L", _I32), ("H", _I32), ("D", _I32), ("io_dtype", _I32),
+                ("reserved", _I32), ("stride", _Pair)]
+
+
+class GdnQkProblem(ctypes.Structure):
+    _fields_ = [("B", _I32), ("L", _I32), ("Hq", _I32), ("Hk", _I32), ("D", _I32),
+                ("io_dtype", _I32), ("norm", _I32), ("pairing", _I32), ("axes", _I32),
+                ("axis_pairs", _I32 * 3), ("shared_positions", _I32), ("eps", ctypes.c_float),
+                ("theta", ctypes.c_double), ("q_stride", _Pair), ("k_stride", _Pair),
+                ("dq_stride", _Pair), ("dk_stride", _Pair)]
+
+
+class GdnLrecProblem(ctypes.Structure):
+    _fields_ = [("B", _I32), ("L", _I32), ("C", _I32), ("io_dtype", _I32), ("flags", _I32),
+                ("reserved", _I32), ("x_stride", _Pair), ("gate_stride", _Pair),
+                ("dx_stride", _Pair), ("dgate_stride", _Pair)]
+
+
+_lib = None
+
+
+def lib():
+    """libgdn.so with the block's prototypes.  Raises if it is not built."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = binding.lib()
+    P = ctypes.POINTER
+    C, size, psize = P(GdnCheckpoint), ctypes.c_size_t, P(ctypes.c_size_t)
+    for name, args in (
+            ("gdn_pack8", [P(GdnPack8Problem), _VP, C, _VP]),
+            ("gdn_unpack8", [P(GdnPack8Problem), C, _VP, _VP]),
+            ("gdn_qk_forward", [P(GdnQkProblem), _VP, _VP, C] + [_VP] * 6 + [C, _VP]),
+            ("gdn_qk_workspace_size", [P(GdnQkProblem), ctypes.c_int, psize]),
+            ("gdn_qk_backward", [P(GdnQkProblem), _VP, _VP, C] + [_VP] * 11 + [size, _VP]),
+            ("gdn_lrec_workspace_size", [P(GdnLrecProblem), ctypes.c_int, psize]),
+            ("gdn_lrec_saved_size", [P(GdnLrecProblem), psize]),
+            ("gdn_lrec_forward", [P(GdnLrecProblem)] + [_VP] * 8 + [size, _VP]),
+            ("gdn_lrec_step", [P(GdnLrecProblem)] + [_VP] * 5),
+            ("gdn_lrec_backward", [P(GdnLrecProblem)] + [_VP] * 11 + [size, _VP])):
+        f = getattr(L, name)
+        f.restype = ctypes.c_int
+        f.argtypes = args
+    _lib = L
+    return L
+
+
+def _device(device):
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def _call(dev, name, *args):
+    """The entry point on `dev`'s current stream, with `dev` current."""
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            _check(f(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+    else:
+        _check(f(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+
+
+def _view(t, name, dtype, shape, dev):
+    """Check a [B, L, ...] tensor whose dimensions behind the tokens are
+    contiguous; returns its strides of batches and tokens (0 where there is
+    one of them)."""
+    if t is None:
+        raise ValueError("%s is required" % name)
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _need(t, name, dtype, shape, dev)
+    st, inner = t.stride(), 1
+    for i in range(len(shape) - 1, 1, -1):
+        if shape[i] != 1 and st[i] != inner:
+            raise ValueError("%s must be contiguous behind its tokens" % name)
+        inner *= shape[i]
+    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+
+
+def _flat(t, name, dtype, shape, dev):
+    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or \
+            not t.is_contiguous():
+        _need(t, name, dtype, shape, dev)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _checkpoint(c, name, shape, dev):
+    _flat(c.values, name + ".values", torch.float8_e4m3fn, shape, dev)
+    _flat(c.scale, name + ".scale", torch.uint8, shape[:-1], dev)
+    return c.values.data_ptr(), c.scale.data_ptr()
+
+
+def _new_checkpoint(shape, dev):
+    return Checkpoint(_empty(shape, torch.float8_e4m3fn, dev),
+                      _empty(shape[:-1], torch.uint8, dev))
+
+
+# ---- 8-bit checkpoints --------------------------------------------------
+
+def _pack8_problem(shape, io, strides):
+    B, L, H, D = shape
+    return GdnPack8Problem(B, L, H, D, GDN_BF16 if io == "bf16" else GDN_FP32, 0,
+                           _Pair(*strides))
+
+
+def pack8(x, out=None):
+    """Checkpoint of x [B, L, H, D] (bf16 or fp32; gdn_pack8)."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, L, H, D]")
+    shape, dev = tuple(x.shape), x.device
+    strides = _view(x, "x", x.dtype, shape, dev)
+    prob = _pack8_problem(shape, _io_of(x), strides)
+    out = out if out is not None else _new_checkpoint(shape, dev)
+    c = GdnCheckpoint(*_checkpoint(out, "out", shape, dev))
+    _call(dev, "gdn_pack8", ctypes.byref(prob), x.data_ptr(), ctypes.byref(c))
+    return out
+
+
+def unpack8(checkpoint, dtype=torch.bfloat16, out=None):
+    """Rows [B, L, H, D] of a checkpoint, in bf16 or fp32 (gdn_unpack8)."""
+    v = checkpoint.values
+    if v.dim() != 4:
+        raise ValueError("checkpoint values must be [B, L, H, D]")
+    shape, dev = tuple(v.shape), v.device
+    c = GdnCheckpoint(*_checkpoint(checkpoint, "checkpoint", shape, dev))
+    out = out if out is not None else _empty(shape, dtype, dev)
+    strides = _view(out, "out", dtype, shape, dev)
+    prob = _pack8_problem(shape, _io_of(out), strides)
+    _call(dev, "gdn_unpack8", ctypes.byref(prob), ctypes.byref(c), out.data_ptr())
+    return out
+
+
+# ---- queries and keys ---------------------------------------------------
+
+def make_qk_problem(B, L, Hq, Hk, D, io="bf16", norm="rms", eps=1e-6, axis_pairs=(),
+                    pairing="halves", theta=10000.0):
+    """gdn_qk_problem with contiguous rows."""
+    pairs = list(axis_pairs)
+    if len(pairs) > 3:
+        raise ValueError("at most 3 axes, got %d" % len(pairs))
+    q, k = _Pair(L * Hq * D, Hq * D), _Pair(L * Hk * D, Hk * D)
+    return GdnQkProblem(B, L, Hq, Hk, D, GDN_BF16 if io == "bf16" else GDN_FP32, NORMS[norm],
+                        PAIRINGS[pairing], len(pairs), (_I32 * 3)(*(pairs + [0] * (3 - len(pairs)))),
+                        0, eps, theta, q, k, _Pair(*q), _Pair(*k))
+
+
+def qk_workspace_size(prob, want_weights):
+    n = ctypes.c_size_t(0)
+    _check(lib().gdn_qk_workspace_size(ctypes.byref(prob), int(want_weights), ctypes.byref(n)),
+           "gdn_qk_workspace_size")
+    return n.value
+
+
+class QkPlan:
+    """Problem, outputs and workspace for repeated gdn_qk_forward /
+    gdn_qk_backward calls on one shape.
+
+    norm: "none", "l2" or "rms".  axis_pairs: rotated pairs of each of a
+    position's coordinates, () for no rotation.  weights: the backward also
+    forms the weights' gradients.  checkpoint: the forward also writes 8-bit
+    checkpoints of the raw rows (``self.checkpoint``, one of q, one of k).
+    backward: allocate the backward's outputs too."""
+
+    def __init__(self, B, L, Hq, Hk, D, io, device, norm="rms", eps=1e-6, axis_pairs=(),
+                 pairing="halves", theta=10000.0, weights=False, checkpoint=False,
+                 backward=False, forward=True):
+        self.prob = make_qk_problem(B, L, Hq, Hk, D, io, norm, eps, axis_pairs, pairing, theta)
+        self._ref = ctypes.byref(self.prob)
+        dev = self.device = _device(device)
+        dt = self.dtype = DTYPES[io]
+        self.q_shape, self.k_shape, self.D = (B, L, Hq, D), (B, L, Hk, D), D
+        self.axes, self.normed = len(axis_pairs), norm != "none"
+        qk_workspace_size(self.prob, False)   # the problem's own checks
+        self.q_out = self.k_out = self.checkpoint = None
+        self._to = None
+        if forward and not backward or checkpoint:
+            self._forward_buffers()
+        if checkpoint:
+            self.checkpoint = tuple(_new_checkpoint(s, dev) for s in (self.q_shape, self.k_shape))
+            self._to = (GdnCheckpoint * 2)(*[GdnCheckpoint(c.values.data_ptr(), c.scale.data_ptr())
+                                             for c in self.checkpoint])
+        self.weights = bool(weights) and self.normed
+        self.dq = self.dk = self.dw = self.ws = None
+        if backward:
+            self._backward_buffers()
+        self._from = (GdnCheckpoint * 2)()
+        self._strides = None
+
+    def _forward_buffers(self):
+        self.q_out = _empty(self.q_shape, self.dtype, self.device)
+        self.k_out = _empty(self.k_shape, self.dtype, self.device)
+
+    def _backward_buffers(self):
+        dev = self.device
+        self.dq = _empty(self.q_shape, self.dtype, dev)
+        self.dk = _empty(self.k_shape, self.dtype, dev)
+        if self.weights:
+            self.dw = _empty((2, self.D), torch.float32, dev)
+            self.ws = _empty(max(16, qk_workspace_size(self.prob, True)), torch.uint8, dev)
+
+    def _set_strides(self, strides):
+        if strides != self._strides:
+            p = self.prob
+            for field, s in zip((p.q_stride, p.k_stride, p.dq_stride, p.dk_stride), strides):
+                field[0], field[1] = s
+            self._strides = strides
+
+    def _source(self, q, k):
+        """(q, k, from) pointers and strides of tensors or checkpoints."""
+        if q is None and k is None and not self.normed:
+            return None, None, None, (0, 0), (0, 0)
+        if isinstance(q, Checkpoint) != isinstance(k, Checkpoint):
+            raise TypeError("q and k must both be tensors or both be checkpoints")
+        if isinstance(q, Checkpoint):
+            f = self._from
+            f[0].values, f[0].scale = _checkpoint(q, "q", self.q_shape, self.device)
+            f[1].values, f[1].scale = _checkpoint(k, "k", self.k_shape, self.device)
+            return None, None, f, (0, 0), (0, 0)
+        qs = _view(q, "q", self.dtype, self.q_shape, self.device)
+        ks = _view(k, "k", self.dtype, self.k_shape, self.device)
+        return q.data_ptr(), k.data_ptr(), None, qs, ks
+
+    def _rest(self, positions, q_weight, k_weight, lengths):
+        B, L, dev = self.q_shape[0], self.q_shape[1], self.device
+        if positions is None and self.axes:
+            raise ValueError("positions are required")
+        if positions is not None:
+            if not self.axes:
+                raise ValueError("positions without axis_pairs")
+            shared = positions.dim() == 2
+            _flat(positions, "positions", torch.int32,
+                  (L, self.axes) if shared else (B, L, self.axes), dev)
+            self.prob.shared_positions = int(shared)
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _flat(w, name, torch.float32, (self.D,), dev)
+        if lengths is not None:
+            _flat(lengths, "lengths", torch.int32, (B,), dev)
+        return _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(lengths)
+
+    def forward(self, q, k, positions=None, q_weight=None, k_weight=None, lengths=None):
+        """q and k (tensors [B, L, H, D], or their checkpoints) normalised,
+        weighted and rotated: the plan's (q_out, k_out)."""
+        qp, kp, src, qs, ks = self._source(q, k)
+        if src is not None and self._to is not None:
+            raise ValueError("a checkpoint cannot be read and written in one call")
+        if qp is None and src is None:
+            raise ValueError("q and k are required")
+        rest = self._rest(positions, q_weight, k_weight, lengths)
+        self._set_strides((qs, ks, (0, 0), (0, 0)))
+        if self.q_out is None:
+            self._forward_buffers()
+        _call(self.device, "gdn_qk_forward", self._ref, qp, kp, src, *rest,
+              self.q_out.data_ptr(), self.k_out.data_ptr(), self._to)
+        return self.q_out, self.k_out
+
+    def backward(self, d_q, d_k, q=None, k=None, positions=None, q_weight=None, k_weight=None,
+                 lengths=None, dq=None, dk=None):
+        """Gradients dict (dq, dk; dq_weight, dk_weight with ``weights``,
+        where the operand has a weight) from those of the outputs.  q, k: the
+        forward's, or their checkpoints (not needed without a norm).  dq, dk:
+        tensors to write, such as slices of the projection's gradient (None:
+        the plan's own)."""
+        dev = self.device
+        qp, kp, src, qs, ks = self._source(q, k)
+        rest = self._rest(positions, q_weight, k_weight, lengths)
+        _flat(d_q, "d_q", self.dtype, self.q_shape, dev)
+        _flat(d_k, "d_k", self.dtype, self.k_shape, dev)
+        if (dq is None or dk is None or self.weights and self.dw is None) and self.dq is None:
+            self._backward_buffers()
+        dq, dk = self.dq if dq is None else dq, self.dk if dk is None else dk
+        dqs = _view(dq, "dq", self.dtype, self.q_shape, dev)
+        dks = _view(dk, "dk", self.dtype, self.k_shape, dev)
+        self._set_strides((qs, ks, dqs, dks))
+        w0 = w1 = ws = None
+        nws = 0
+        if self.weights:
+            w0 = self.dw.data_ptr()
+            w1, ws, nws = w0 + 4 * self.D, self.ws.data_ptr(), self.ws.numel()
+        _call(dev, "gdn_qk_backward", self._ref, qp, kp, src, *rest, d_q.data_ptr(),
+              d_k.data_ptr(), dq.data_ptr(), dk.data_ptr(), w0, w1, ws, nws)
+        out = {"dq": dq, "dk": dk}
+        if self.weights:
+            if q_weight is not None:
+                out["dq_weight"] = self.dw[0]
+            if k_weight is not None:
+                out["dk_weight"] = self.dw[1]
+        return out
+
+
+def _qk_dims(q, k):
+    a, b = (t.values if isinstance(t, Checkpoint) else t for t in (q, k))
+    if a.dim() != 4 or b.dim() != 4:
+        raise ValueError("q and k must be [B, L, H, D]")
+    B, L, Hq, D = a.shape
+    if tuple(b.shape[:2]) != (B, L) or b.shape[3] != D:
+        raise ValueError("k has shape %s, expected [%d, %d, heads, %d]" % (tuple(b.shape), B, L, D))
+    return (B, L, Hq, b.shape[2], D), a.device
+
+
+def qk_forward(q, k, positions=None, q_weight=None, k_weight=None, lengths=None, norm="rms",
+               eps=1e-6, axis_pairs=(), pairing="halves", theta=10000.0, checkpoint=False,
+               dtype=None):
+    """(q_out, k_out) of gdn_qk_forward; with ``checkpoint`` also the pair of
+    8-bit checkpoints.  From checkpoints, ``dtype`` is the outputs'."""
+    dims, dev = _qk_dims(q, k)
+    io = _io_of(q) if dtype is None and not isinstance(q, Checkpoint) else \
+        {v: n for n, v in DTYPES.items()}[dtype or torch.bfloat16]
+    plan = QkPlan(*dims, io, dev, norm, eps, axis_pairs, pairing, theta, checkpoint=checkpoint)
+    out = plan.forward(q, k, positions, q_weight, k_weight, lengths)
+    return out + (plan.checkpoint,) if checkpoint else out
+
+
+def qk_backward(d_q, d_k, q=None, k=None, positions=None, q_weight=None, k_weight=None,
+                lengths=None, norm="rms", eps=1e-6, axis_pairs=(), pairing="halves",
+                theta=10000.0, dq=None, dk=None):
+    """Gradients dict of gdn_qk_backward (see QkPlan.backward)."""
+    dims, dev = _qk_dims(d_q, d_k)
+    plan = QkPlan(*dims, _io_of(d_q), dev, norm, eps, axis_pairs, pairing, theta,
+                  weights=q_weight is not None or k_weight is not None, forward=False)
+    return plan.backward(d_q, d_k, q, k, positions, q_weight, k_weight, lengths, dq, dk)
+
+
+# ---- gated linear recurrence --------------------------------------------
+
+def make_lrec_problem(B, L, C, io="bf16", gate_logits=False, complement=False):
+    """gdn_lrec_problem with contiguous tensors."""
+    s = (L * C, C)
+    return GdnLrecProblem(B, L, C, GDN_BF16 if io == "bf16" else GDN_FP32,
+                          (binding.GDN_FLAG_GATE_LOGITS if gate_logits else 0) |
+                          (GDN_LREC_COMPLEMENT if complement else 0), 0,
+                          _Pair(*s), _Pair(*s), _Pair(*s), _Pair(*s))
+
+
+def lrec_workspace_size(prob, op):
+    n = ctypes.c_size_t(0)
+    _check(lib().gdn_lrec_workspace_size(ctypes.byref(prob), int(op), ctypes.byref(n)),
+           "gdn_lrec_workspace_size")
+    return n.value
+
+
+def lrec_saved_size(prob):
+    n = ctypes.c_size_t(0)
+    _check(lib().gdn_lrec_saved_size(ctypes.byref(prob), ctypes.byref(n)), "gdn_lrec_saved_size")
+    return n.value
+
+
+class LrecPlan:
+    """Problem, outputs and workspace for repeated gdn_lrec_forward /
+    gdn_lrec_step / gdn_lrec_backward calls on one shape.  saved: the forward
+    fills ``self.saved`` for the backward.  backward: allocate the backward's
+    outputs and workspace too."""
+
+    def __init__(self, B, L, C, io, device, gate_logits=False, complement=False, saved=False,
+                 backward=False, forward=True):
+        self.prob = make_lrec_problem(B, L, C, io, gate_logits, complement)
+        self._ref = ctypes.byref(self.prob)
+        dev = self.device = _device(device)
+        dt = self.dtype = DTYPES[io]
+        self.shape, self.state_shape = (B, L, C), (B, C)
+        self.o = self.state_out = self.dx = self.dgate = self.dstate_in = None
+        n = max([16] + [lrec_workspace_size(self.prob, op) for op, want in
+                        ((GDN_OP_FORWARD, forward), (GDN_OP_BACKWARD, backward)) if want])
+        self.ws = _empty((n,), torch.uint8, dev)
+        if forward:
+            self.o = _empty(self.shape, dt, dev)
+            self.state_out = _empty(self.state_shape, torch.float32, dev)
+        self.saved = _empty((lrec_saved_size(self.prob),), torch.uint8, dev) if saved else None
+        if backward:
+            self.dx = _empty(self.shape, dt, dev)
+            self.dgate = _empty(self.shape, dt, dev)
+            self.dstate_in = _empty(self.state_shape, torch.float32, dev)
+        self._strides = None
+
+    def _set_strides(self, strides):
+        if strides != self._strides:
+            p = self.prob
+            for field, s in zip((p.x_stride, p.gate_stride, p.dx_stride, p.dgate_stride), strides):
+                field[0], field[1] = s
+            self._strides = strides
+
+    def _inputs(self, x, gate, lengths, states):
+        dev = self.device
+        xs = _view(x, "x", self.dtype, self.shape, dev)
+        gs = _view(gate, "gate", self.dtype, self.shape, dev)
+        if lengths is not None:
+            _flat(lengths, "lengths", torch.int32, self.shape[:1], dev)
+        for t, name in states:
+            if t is not None:
+                _flat(t, name, torch.float32, self.state_shape, dev)
+        return xs, gs
+
+    def forward(self, x, gate, state=None, lengths=None, state_out=None):
+        """(o, state_out) of gdn_lrec_forward.  state_out: None (the plan's
+        own buffer) or a [B, C] fp32 tensor, which may be `state` itself."""
+        if self.o is None:
+            raise ValueError("the plan was made without forward")
+        strides = self._inputs(x, gate, lengths, ((state, "state"), (state_out, "state_out")))
+        self._set_strides(strides + ((0, 0), (0, 0)))
+        so = self.state_out if state_out is None else state_out
+        _call(self.device, "gdn_lrec_forward", self._ref, x.data_ptr(), gate.data_ptr(),
+              _ptr(lengths), _ptr(state), self.o.data_ptr(), so.data_ptr(), _ptr(self.saved),
+              self.ws.data_ptr(), self.ws.numel())
+        return self.o, so
+
+    def step(self, x, gate, state):
+        """o of gdn_lrec_step (one token): `state` [B, C] is updated in place."""
+        if self.o is None:
+            raise ValueError("the plan was made without forward")
+        if state is None:
+            raise ValueError("state is required")
+        strides = self._inputs(x, gate, None, ((state, "state"),))
+        self._set_strides(strides + ((0, 0), (0, 0)))
+        _call(self.device, "gdn_lrec_step", self._ref, x.data_ptr(), gate.data_ptr(),
+              state.data_ptr(), self.o.data_ptr())
+        return self.o
+
+    def backward(self, x, gate, d_o, state=None, d_state=None, lengths=None, saved=None, dx=None,
+                 dgate=None):
+        """Gradients dict (dx, dgate, dstate_in) of gdn_lrec_backward.  saved:
+        the forward's buffer, or None to form it again.  dx, dgate: tensors to
+        write, such as slices of one gradient (None: the plan's own)."""
+        dev = self.device
+        if self.dstate_in is None:
+            raise ValueError("the plan was made without backward")
+        strides = self._inputs(x, gate, lengths, ((state, "state"), (d_state, "d_state")))
+        _flat(d_o, "d_o", self.dtype, self.shape, dev)
+        if saved is not None:
+            _flat(saved, "saved", torch.uint8, (lrec_saved_size(self.prob),), dev)
+        dx, dgate = self.dx if dx is None else dx, self.dgate if dgate is None else dgate
+        self._set_strides(strides + (_view(dx, "dx", self.dtype, self.shape, dev),
+                                     _view(dgate, "dgate", self.dtype, self.shape, dev)))
+        _call(dev, "gdn_lrec_backward", self._ref, x.data_ptr(), gate.data_ptr(), _ptr(lengths),
+              _ptr(state), d_o.data_ptr(), _ptr(d_state), _ptr(saved), dx.data_ptr(),
+              dgate.data_ptr(), self.dstate_in.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        return {"dx": dx, "dgate": dgate, "dstate_in": self.dstate_in}
+
+
+def _lrec_dims(x):
+    if x.dim() != 3:
+        raise ValueError("x must be [B, L, C]")
+    return tuple(x.shape) + (_io_of(x), x.device)
+
+
+def lrec_forward(x, gate, state=None, lengths=None, gate_logits=False, complement=False,
+                 return_saved=False):
+    """o, state_out (and the saved buffer) of gdn_lrec_forward."""
+    plan = LrecPlan(*_lrec_dims(x), gate_logits, complement, return_saved)
+    out = plan.forward(x, gate, state, lengths)
+    return out + (plan.saved,) if return_saved else out
+
+
+def lrec_step(x, gate, state, gate_logits=False, complement=False):
+    """One token, x and gate [B, 1, C]; `state` [B, C] fp32 is updated in place."""
+    return LrecPlan(*_lrec_dims(x), gate_logits, complement).step(x, gate, state)
+
+
+def lrec_backward(x, gate, d_o, state=None, d_state=None, lengths=None, saved=None,
+                  gate_logits=False, complement=False):
+    """Gradients dict of gdn_lrec_backward."""
+    plan = LrecPlan(*_lrec_dims(x), gate_logits, complement, backward=True, forward=False)
+    return plan.backward(x, gate, d_o, state, d_state, lengths, saved)

@@ -1,0 +1,625 @@
+// Host side of the block's operators (include/gdn_block.h): argument
+// validation, workspace carving and dispatch onto the caller's stream.
+#include <math.h>
+#include <stdint.h>
+
+#include "gdn_block.h"
+#include "gdn_block_internal.h"
+
+using namespace gdn;
+
+namespace {
+
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int bytes_of(int io) { return io == IO_BF16 ? 2 : 4; }
+
+// A tensor as an operand: `rows` of the innermost `width` bytes at p + b sb +
+// l sl.  Contiguous buffers are one row.
+struct Region {
+  const void* p;
+  int64_t width;
+  int64_t B, sb, L, sl;   // strides in bytes
+};
+Region flat(const void* p, int64_t bytes) { return Region{p, bytes, 1, 0, 1, 0}; }
+
+int64_t gcd(int64_t a, int64_t b) {
+  while (b) {
+    const int64_t t = a % b;
+    a = b;
+    b = t;
+  }
+  return a;
+}
+
+// Whether two regions may share a byte.  Their extents first; where those
+// meet, both sets of rows repeat with a period that divides every stride
+// (their gcd), so rows that are apart within one period are apart
+// everywhere: interleaved views of one allocation.
+bool meet(const Region& a, const Region& b) {
+  if (!a.p || !b.p || a.width <= 0 || b.width <= 0) return false;
+  const int64_t a0 = (int64_t)(uintptr_t)a.p, b0 = (int64_t)(uintptr_t)b.p;
+  const int64_t a1 = a0 + (a.B - 1) * a.sb + (a.L - 1) * a.sl + a.width;
+  const int64_t b1 = b0 + (b.B - 1) * b.sb + (b.L - 1) * b.sl + b.width;
+  if (a1 <= b0 || b1 <= a0) return false;
+  int64_t period = 0;
+  if (a.B > 1) period = gcd(period, a.sb);
+  if (a.L > 1) period = gcd(period, a.sl);
+  if (b.B > 1) period = gcd(period, b.sb);
+  if (b.L > 1) period = gcd(period, b.sl);
+  if (period == 0) return true;
+  int64_t off = (b0 - a0) % period;
+  if (off < 0) off += period;
+  return !(off >= a.width && off + b.width <= period);
+}
+
+bool any_meet(const Region* outs, int no, const Region* ins, int ni) {
+  for (int i = 0; i < no; ++i) {
+    for (int j = 0; j < ni; ++j)
+      if (meet(outs[i], ins[j])) return true;
+    for (int j = i + 1; j < no; ++j)
+      if (meet(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
+// Rows of `width` elements at these strides do not overlap each other.
+bool rows_apart(int64_t B, int64_t L, int64_t width, const int64_t* stride) {
+  const int64_t sb = stride[0], sl = stride[1];
+  if (L > 1 && sl < width) return false;
+  if (B > 1 && sb < width) return false;
+  if (B > 1 && L > 1) {
+    // one of the two axes steps over the whole of the other
+    return sb >= (L - 1) * sl + width || sl >= (B - 1) * sb + width;
+  }
+  return true;
+}
+
+gdn_status check_stride(const int64_t* s) {
+  return s[0] < 0 || s[1] < 0 || s[0] > kMaxStride || s[1] > kMaxStride ? GDN_ERR_BAD_SHAPE
+                                                                        : GDN_OK;
+}
+
+// Furthest element of a strided tensor within what 64-bit byte offsets and
+// the documented limit allow.
+bool reaches(int64_t B, int64_t L, int64_t width, const int64_t* s) {
+  if (B > 1 && s[0] > 2 * kMaxElements / (B - 1)) return false;
+  if (L > 1 && s[1] > 2 * kMaxElements / (L - 1)) return false;
+  return (B - 1) * s[0] + (L - 1) * s[1] + width <= 2 * kMaxElements;
+}
+
+gdn_status hip_status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_HIP; }
+
+Region strided(const void* p, int64_t B, int64_t L, int64_t width, const int64_t* s, int es) {
+  return Region{p, width * es, B, s[0] * es, L, s[1] * es};
+}
+
+// Whether pieces of V elements fit a row's layout, its strides and pointers.
+struct RowUse {
+  const void* p;
+  const int64_t* stride;   // nullptr: contiguous rows of D
+  int es;
+};
+bool fits(int V, int B, int L, int D, int pairs, const RowUse* use, int n) {
+  if (D % (2 * V) || pairs % V) return false;
+  for (int i = 0; i < n; ++i) {
+    if (!use[i].p) continue;
+    if (!aligned(use[i].p, V * use[i].es)) return false;
+    const int64_t* st = use[i].stride;   // a stride counts where there is a second row
+    if (st && ((B > 1 && st[0] % V) || (L > 1 && st[1] % V))) return false;
+  }
+  return true;
+}
+// The widest pieces that fit: 16 bytes of the io type where rows allow, else
+// 8 or 4 (bf16) or 8 (fp32); 0 if none do.
+RowShape row_shape(int B, int L, int D, int pairs, int io, const RowUse* use, int n) {
+  RowShape r{D, 0, 0, 0};
+  for (int V = io == IO_BF16 ? 8 : 4; V >= 2 && !r.V; V /= 2)
+    if (fits(V, B, L, D, pairs, use, n)) r.V = V;
+  if (!r.V) return r;
+  r.lanes = D / (2 * r.V);
+  for (r.group = 1; r.group < r.lanes;) r.group *= 2;
+  return r;
+}
+
+// ---- pack8 ----
+struct Pack {
+  int io, es;
+};
+gdn_status check_pack(const gdn_pack8_problem* p, Pack* s) {
+  if (!p) return GDN_ERR_NULL_POINTER;
+  if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_FP32) return GDN_ERR_BAD_DTYPE;
+  if (p->B < 1 || p->L < 1 || p->H < 1 || p->D < 1) return GDN_ERR_BAD_SHAPE;
+  if (p->D % 4 || p->D > kRowMaxD || p->reserved) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)p->B * p->L > INT32_MAX || (int64_t)p->B * p->L * p->H > INT32_MAX)
+    return GDN_ERR_BAD_SHAPE;
+  gdn_status st = check_stride(p->stride);
+  if (st != GDN_OK) return st;
+  if (!reaches(p->B, p->L, (int64_t)p->H * p->D, p->stride)) return GDN_ERR_BAD_SHAPE;
+  s->io = p->io_dtype == GDN_BF16 ? IO_BF16 : IO_F32;
+  s->es = bytes_of(s->io);
+  return GDN_OK;
+}
+
+gdn_status pack_args(const gdn_pack8_problem* p, const Pack& s, const void* x,
+                     const gdn_checkpoint* c, PackArgs* a) {
+  const RowUse use[] = {{x, p->stride, s.es}, {c->values, nullptr, 1}};
+  a->row = row_shape(p->B, p->L, p->D, 0, s.io, use, 2);
+  if (!a->row.V) return GDN_ERR_MISALIGNED;
+  a->x = RowView{x, p->stride[0], p->stride[1]};
+  a->v = c->values;
+  a->scale = c->scale;
+  a->B = p->B;
+  a->L = p->L;
+  a->H = p->H;
+  return GDN_OK;
+}
+
+// ---- qk ----
+struct Qk {
+  int io, es, pairs;
+};
+gdn_status check_qk(const gdn_qk_problem* p, Qk* s) {
+  if (!p) return GDN_ERR_NULL_POINTER;
+  if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_FP32) return GDN_ERR_BAD_DTYPE;
+  if (p->B < 1 || p->L < 1 || p->Hq < 1 || p->Hk < 1 || p->D < 1) return GDN_ERR_BAD_SHAPE;
+  if (p->D % 4 || p->D > kRowMaxD) return GDN_ERR_UNSUPPORTED;
+  if (p->norm < GDN_NORM_NONE || p->norm > GDN_NORM_RMS) return GDN_ERR_UNSUPPORTED;
+  if (p->pairing != GDN_PAIR_HALVES && p->pairing != GDN_PAIR_ADJACENT)
+    return GDN_ERR_UNSUPPORTED;
+  if (p->shared_positions != 0 && p->shared_positions != 1) return GDN_ERR_UNSUPPORTED;
+  const int64_t heads = (int64_t)p->Hq + p->Hk, tokens = (int64_t)p->B * p->L;
+  if (tokens > INT32_MAX || tokens * heads > INT32_MAX) return GDN_ERR_BAD_SHAPE;
+  if (heads * p->D > INT32_MAX / 4) return GDN_ERR_BAD_SHAPE;
+  if (!isfinite(p->eps) || p->eps < 0.f) return GDN_ERR_BAD_SHAPE;
+  if (p->axes < 0 || p->axes > 3) return GDN_ERR_BAD_SHAPE;
+  int64_t pairs = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (i < p->axes ? p->axis_pairs[i] < 1 : p->axis_pairs[i] != 0) return GDN_ERR_BAD_SHAPE;
+    pairs += p->axis_pairs[i];
+  }
+  if (pairs % 2 || 2 * pairs > p->D) return GDN_ERR_BAD_SHAPE;
+  if (pairs && !(isfinite(p->theta) && p->theta > 0.0)) return GDN_ERR_BAD_SHAPE;
+  const int64_t* strides[] = {p->q_stride, p->k_stride, p->dq_stride, p->dk_stride};
+  for (int i = 0; i < 4; ++i) {
+    gdn_status st = check_stride(strides[i]);
+    if (st != GDN_OK) return st;
+    if (!reaches(p->B, p->L, (int64_t)(i & 1 ? p->Hk : p->Hq) * p->D, strides[i]))
+      return GDN_ERR_BAD_SHAPE;
+  }
+  s->io = p->io_dtype == GDN_BF16 ? IO_BF16 : IO_F32;
+  s->es = bytes_of(s->io);
+  s->pairs = (int)pairs;
+  return GDN_OK;
+}
+
+void qk_args(const gdn_qk_problem* p, const Qk& s, QkArgs* a) {
+  a->B = p->B;
+  a->L = p->L;
+  a->H[0] = p->Hq;
+  a->H[1] = p->Hk;
+  a->norm = p->norm;
+  a->adjacent = p->pairing == GDN_PAIR_ADJACENT;
+  a->axes = p->axes;
+  a->pairs = s.pairs;
+  a->bound1 = p->axis_pairs[0];
+  a->bound2 = p->axis_pairs[0] + p->axis_pairs[1];
+  a->pos_shared = p->shared_positions;
+  a->eps = p->eps;
+  a->c = p->norm == GDN_NORM_RMS ? 1.f / (float)p->D : 1.f;
+  int m = 0;
+  for (int axis = 0; axis < p->axes; ++axis)
+    for (int f = 0; f < p->axis_pairs[axis]; ++f)
+      a->turns[m++] = pow(p->theta, -(double)f / p->axis_pairs[axis]) / (2.0 * M_PI);
+}
+
+struct QkRegions {
+  int64_t rq, rk, nq, nk;   // rows, elements
+};
+QkRegions qk_regions(const gdn_qk_problem* p) {
+  QkRegions r;
+  r.rq = (int64_t)p->B * p->L * p->Hq;
+  r.rk = (int64_t)p->B * p->L * p->Hk;
+  r.nq = r.rq * p->D;
+  r.nk = r.rk * p->D;
+  return r;
+}
+
+bool whole(const gdn_checkpoint* c) {
+  return c[0].values && c[0].scale && c[1].values && c[1].scale;
+}
+
+// ---- lrec ----
+struct Lrec {
+  int io, es;
+  int64_t chunks;
+};
+gdn_status check_lrec(const gdn_lrec_problem* p, Lrec* s) {
+  if (!p) return GDN_ERR_NULL_POINTER;
+  if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_FP32) return GDN_ERR_BAD_DTYPE;
+  if (p->B < 1 || p->L < 1 || p->C < 1) return GDN_ERR_BAD_SHAPE;
+  if ((p->flags & ~(GDN_FLAG_GATE_LOGITS | GDN_LREC_COMPLEMENT)) || p->reserved)
+    return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)p->B * p->L > INT32_MAX || p->L > INT32_MAX - 2 * kLrecChunk ||
+      p->C > INT32_MAX - 256 || (int64_t)p->B * p->L > kMaxElements / p->C)
+    return GDN_ERR_BAD_SHAPE;
+  const int64_t* strides[] = {p->x_stride, p->gate_stride, p->dx_stride, p->dgate_stride};
+  for (int i = 0; i < 4; ++i) {
+    gdn_status st = check_stride(strides[i]);
+    if (st != GDN_OK) return st;
+    if (!reaches(p->B, p->L, p->C, strides[i])) return GDN_ERR_BAD_SHAPE;
+  }
+  s->io = p->io_dtype == GDN_BF16 ? IO_BF16 : IO_F32;
+  s->es = bytes_of(s->io);
+  s->chunks = (p->L + kLrecChunk - 1) / kLrecChunk;
+  // a launch's workgroups at one channel a lane, and their threads
+  const int64_t strips = ((int64_t)p->C + 63) / 64;
+  if (s->chunks * p->B > ((int64_t(1) << 32) - 1) / 512 / strips) return GDN_ERR_BAD_SHAPE;
+  return GDN_OK;
+}
+int64_t lrec_chunk_bytes(const gdn_lrec_problem* p, const Lrec& s) {
+  return (s.chunks * p->B * p->C * 4 + 255) / 256 * 256;
+}
+int64_t lrec_ws(const gdn_lrec_problem* p, const Lrec& s, int op) {
+  // the chunks' maps (A, H), and the entering states where no saved buffer
+  // is given
+  if (op == GDN_OP_STEP) return 0;
+  if (op == GDN_OP_FORWARD && s.chunks == 1) return 0;
+  return 3 * lrec_chunk_bytes(p, s);
+}
+
+struct LrecUse {
+  const void* p;
+  const int64_t* stride;
+};
+// The widest vector of at most `most` elements that the channels, strides and
+// pointers allow.
+int lrec_vec(const gdn_lrec_problem* p, int es, int most, const LrecUse* use, int n) {
+  if (p->C % most) return 1;
+  for (int i = 0; i < n; ++i) {
+    if (!aligned(use[i].p, most * es)) return 1;
+    const int64_t* st = use[i].stride;
+    if (st && ((p->B > 1 && st[0] % most) || (p->L > 1 && st[1] % most))) return 1;
+  }
+  return most;
+}
+
+void lrec_args(const gdn_lrec_problem* p, const Lrec& s, int vec, LrecArgs* a) {
+  a->B = p->B;
+  a->L = p->L;
+  a->C = p->C;
+  a->chunks = (int)s.chunks;
+  a->strips = (int)(((int64_t)p->C + 64 * vec - 1) / (64 * vec));
+  a->logits = (p->flags & GDN_FLAG_GATE_LOGITS) != 0;
+  a->complement = (p->flags & GDN_LREC_COMPLEMENT) != 0;
+  a->x_sb = p->x_stride[0];
+  a->x_sl = p->x_stride[1];
+  a->z_sb = p->gate_stride[0];
+  a->z_sl = p->gate_stride[1];
+}
+
+gdn_status run_lrec_forward(const gdn_lrec_problem* p, const Lrec& s, const void* x,
+                            const void* gate, const int32_t* lengths, const float* state_in,
+                            void* o, float* state_out, void* saved, void* workspace,
+                            hipStream_t stream) {
+  const LrecUse use[] = {{x, p->x_stride}, {gate, p->gate_stride}, {o, nullptr}};
+  const int vec = lrec_vec(p, s.es, 4, use, 3);
+  LrecArgs a{};
+  lrec_args(p, s, vec, &a);
+  a.x = x;
+  a.z = gate;
+  a.len = lengths;
+  a.h0 = state_in;
+  a.o = o;
+  a.hT = state_out;
+  if (s.chunks > 1) {
+    char* ws = static_cast<char*>(workspace);
+    const int64_t n = lrec_chunk_bytes(p, s);
+    a.compA = reinterpret_cast<float*>(ws);
+    a.compH = reinterpret_cast<float*>(ws + n);
+    a.enter = reinterpret_cast<float*>(ws + 2 * n);
+  }
+  if (saved) a.enter = static_cast<float*>(saved);
+  return hip_status(launch_lrec_forward(a, s.io, vec, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_pack8(const gdn_pack8_problem* p, const void* x, const gdn_checkpoint* to,
+                     void* stream) {
+  Pack s;
+  gdn_status st = check_pack(p, &s);
+  if (st != GDN_OK) return st;
+  if (!x || !to || !to->values || !to->scale) return GDN_ERR_NULL_POINTER;
+  PackArgs a{};
+  st = pack_args(p, s, x, to, &a);
+  if (st != GDN_OK) return st;
+  const int64_t rows = (int64_t)p->B * p->L * p->H;
+  const Region ins[] = {strided(x, p->B, p->L, (int64_t)p->H * p->D, p->stride, s.es)};
+  const Region outs[] = {flat(to->values, rows * p->D), flat(to->scale, rows)};
+  if (any_meet(outs, 2, ins, 1)) return GDN_ERR_ALIASING;
+  return hip_status(launch_pack8(a, s.io, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_unpack8(const gdn_pack8_problem* p, const gdn_checkpoint* from, void* x,
+                       void* stream) {
+  Pack s;
+  gdn_status st = check_pack(p, &s);
+  if (st != GDN_OK) return st;
+  if (!x || !from || !from->values || !from->scale) return GDN_ERR_NULL_POINTER;
+  if (!rows_apart(p->B, p->L, (int64_t)p->H * p->D, p->stride)) return GDN_ERR_BAD_SHAPE;
+  PackArgs a{};
+  st = pack_args(p, s, x, from, &a);
+  if (st != GDN_OK) return st;
+  const int64_t rows = (int64_t)p->B * p->L * p->H;
+  const Region outs[] = {strided(x, p->B, p->L, (int64_t)p->H * p->D, p->stride, s.es)};
+  const Region ins[] = {flat(from->values, rows * p->D), flat(from->scale, rows)};
+  if (any_meet(outs, 1, ins, 2)) return GDN_ERR_ALIASING;
+  return hip_status(launch_unpack8(a, s.io, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_qk_forward(const gdn_qk_problem* p, const void* q, const void* k,
+                          const gdn_checkpoint* from, const float* q_weight,
+                          const float* k_weight, const int32_t* positions,
+                          const int32_t* lengths, void* q_out, void* k_out,
+                          const gdn_checkpoint* to, void* stream) {
+  Qk s;
+  gdn_status st = check_qk(p, &s);
+  if (st != GDN_OK) return st;
+  if (from ? (q || k) : (!q || !k)) return GDN_ERR_NULL_POINTER;
+  if (from && !whole(from)) return GDN_ERR_NULL_POINTER;
+  if (to && !whole(to)) return GDN_ERR_NULL_POINTER;
+  if (!q_out || !k_out || (p->axes && !positions)) return GDN_ERR_NULL_POINTER;
+  if (from && to) return GDN_ERR_UNSUPPORTED;
+  if (p->norm == GDN_NORM_NONE && (q_weight || k_weight)) return GDN_ERR_UNSUPPORTED;
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(positions, 4) ||
+      !aligned(lengths, 4))
+    return GDN_ERR_MISALIGNED;
+  QkArgs a{};
+  qk_args(p, s, &a);
+  const RowUse use[] = {{q, p->q_stride, s.es},
+                        {k, p->k_stride, s.es},
+                        {q_out, nullptr, s.es},
+                        {k_out, nullptr, s.es},
+                        {from ? from[0].values : nullptr, nullptr, 1},
+                        {from ? from[1].values : nullptr, nullptr, 1},
+                        {to ? to[0].values : nullptr, nullptr, 1},
+                        {to ? to[1].values : nullptr, nullptr, 1}};
+  a.row = row_shape(p->B, p->L, p->D, s.pairs, s.io, use, 8);
+  if (!a.row.V) return GDN_ERR_MISALIGNED;
+  const QkRegions r = qk_regions(p);
+  const int64_t tokens = (int64_t)p->B * p->L;
+  const Region ins[] = {
+      strided(q, p->B, p->L, (int64_t)p->Hq * p->D, p->q_stride, s.es),
+      strided(k, p->B, p->L, (int64_t)p->Hk * p->D, p->k_stride, s.es),
+      flat(from ? from[0].values : nullptr, r.nq), flat(from ? from[1].values : nullptr, r.nk),
+      flat(from ? from[0].scale : nullptr, r.rq), flat(from ? from[1].scale : nullptr, r.rk),
+      flat(q_weight, p->D * 4), flat(k_weight, p->D * 4),
+      flat(positions, (p->shared_positions ? (int64_t)p->L : tokens) * p->axes * 4),
+      flat(lengths, (int64_t)p->B * 4)};
+  const Region outs[] = {
+      flat(q_out, r.nq * s.es), flat(k_out, r.nk * s.es),
+      flat(to ? to[0].values : nullptr, r.nq), flat(to ? to[1].values : nullptr, r.nk),
+      flat(to ? to[0].scale : nullptr, r.rq), flat(to ? to[1].scale : nullptr, r.rk)};
+  if (any_meet(outs, 6, ins, 10)) return GDN_ERR_ALIASING;
+  a.x[0] = RowView{q, p->q_stride[0], p->q_stride[1]};
+  a.x[1] = RowView{k, p->k_stride[0], p->k_stride[1]};
+  for (int i = 0; i < 2; ++i) {
+    if (from) {
+      a.v8[i] = static_cast<const uint8_t*>(from[i].values);
+      a.s8[i] = static_cast<const uint8_t*>(from[i].scale);
+    }
+    if (to) {
+      a.v8_out[i] = static_cast<uint8_t*>(to[i].values);
+      a.s8_out[i] = static_cast<uint8_t*>(to[i].scale);
+    }
+  }
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.pos = positions;
+  a.len = lengths;
+  a.y[0] = q_out;
+  a.y[1] = k_out;
+  return hip_status(
+      launch_qk_forward(a, s.io, from != nullptr, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_qk_workspace_size(const gdn_qk_problem* p, int want_weights, size_t* bytes) {
+  if (!bytes) return GDN_ERR_NULL_POINTER;
+  Qk s;
+  gdn_status st = check_qk(p, &s);
+  if (st != GDN_OK) return st;
+  *bytes = want_weights
+               ? (size_t)qk_backward_wgs((int64_t)p->B * p->L) * 2 * p->D * sizeof(float)
+               : 0;
+  return GDN_OK;
+}
+
+gdn_status gdn_qk_backward(const gdn_qk_problem* p, const void* q, const void* k,
+                           const gdn_checkpoint* from, const float* q_weight,
+                           const float* k_weight, const int32_t* positions,
+                           const int32_t* lengths, const void* d_qout, const void* d_kout,
+                           void* dq, void* dk, float* dq_weight, float* dk_weight,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  Qk s;
+  gdn_status st = check_qk(p, &s);
+  if (st != GDN_OK) return st;
+  const bool normed = p->norm != GDN_NORM_NONE;
+  if (from ? (q || k) : normed && (!q || !k)) return GDN_ERR_NULL_POINTER;
+  if (from && !whole(from)) return GDN_ERR_NULL_POINTER;
+  if (!d_qout || !d_kout || !dq || !dk || (p->axes && !positions)) return GDN_ERR_NULL_POINTER;
+  if (!dq_weight != !dk_weight) return GDN_ERR_NULL_POINTER;
+  if (dq_weight && !workspace) return GDN_ERR_NULL_POINTER;
+  if (!normed && (q_weight || k_weight || dq_weight)) return GDN_ERR_UNSUPPORTED;
+  const int64_t hq = (int64_t)p->Hq * p->D, hk = (int64_t)p->Hk * p->D;
+  if (!rows_apart(p->B, p->L, hq, p->dq_stride) || !rows_apart(p->B, p->L, hk, p->dk_stride))
+    return GDN_ERR_BAD_SHAPE;
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(positions, 4) ||
+      !aligned(lengths, 4) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4) ||
+      !aligned(workspace, 16))
+    return GDN_ERR_MISALIGNED;
+  const int64_t need =
+      dq_weight ? (int64_t)qk_backward_wgs((int64_t)p->B * p->L) * 2 * p->D * 4 : 0;
+  if (need && workspace_bytes < (size_t)need) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  QkArgs a{};
+  qk_args(p, s, &a);
+  const RowUse use[] = {{q, p->q_stride, s.es},
+                        {k, p->k_stride, s.es},
+                        {d_qout, nullptr, s.es},
+                        {d_kout, nullptr, s.es},
+                        {dq, p->dq_stride, s.es},
+                        {dk, p->dk_stride, s.es},
+                        {from ? from[0].values : nullptr, nullptr, 1},
+                        {from ? from[1].values : nullptr, nullptr, 1}};
+  a.row = row_shape(p->B, p->L, p->D, s.pairs, s.io, use, 8);
+  if (!a.row.V) return GDN_ERR_MISALIGNED;
+  const QkRegions r = qk_regions(p);
+  const int64_t tokens = (int64_t)p->B * p->L;
+  const Region ins[] = {
+      strided(q, p->B, p->L, hq, p->q_stride, s.es),
+      strided(k, p->B, p->L, hk, p->k_stride, s.es),
+      flat(from ? from[0].values : nullptr, r.nq), flat(from ? from[1].values : nullptr, r.nk),
+      flat(from ? from[0].scale : nullptr, r.rq), flat(from ? from[1].scale : nullptr, r.rk),
+      flat(q_weight, p->D * 4), flat(k_weight, p->D * 4),
+      flat(positions, (p->shared_positions ? (int64_t)p->L : tokens) * p->axes * 4),
+      flat(lengths, (int64_t)p->B * 4), flat(d_qout, r.nq * s.es), flat(d_kout, r.nk * s.es)};
+  const Region outs[] = {strided(dq, p->B, p->L, hq, p->dq_stride, s.es),
+                         strided(dk, p->B, p->L, hk, p->dk_stride, s.es),
+                         flat(dq_weight, p->D * 4), flat(dk_weight, p->D * 4),
+                         flat(need ? workspace : nullptr, need)};
+  if (any_meet(outs, 5, ins, 12)) return GDN_ERR_ALIASING;
+  a.x[0] = RowView{q, p->q_stride[0], p->q_stride[1]};
+  a.x[1] = RowView{k, p->k_stride[0], p->k_stride[1]};
+  a.dx[0] = RowView{dq, p->dq_stride[0], p->dq_stride[1]};
+  a.dx[1] = RowView{dk, p->dk_stride[0], p->dk_stride[1]};
+  for (int i = 0; from && i < 2; ++i) {
+    a.v8[i] = static_cast<const uint8_t*>(from[i].values);
+    a.s8[i] = static_cast<const uint8_t*>(from[i].scale);
+  }
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.pos = positions;
+  a.len = lengths;
+  a.y[0] = const_cast<void*>(d_qout);
+  a.y[1] = const_cast<void*>(d_kout);
+  a.part = dq_weight ? static_cast<float*>(workspace) : nullptr;
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  return hip_status(
+      launch_qk_backward(a, s.io, from != nullptr, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_lrec_workspace_size(const gdn_lrec_problem* p, int op, size_t* bytes) {
+  if (!bytes) return GDN_ERR_NULL_POINTER;
+  Lrec s;
+  gdn_status st = check_lrec(p, &s);
+  if (st != GDN_OK) return st;
+  if (op < GDN_OP_FORWARD || op > GDN_OP_BACKWARD) return GDN_ERR_BAD_SHAPE;
+  if (op == GDN_OP_STEP && p->L != 1) return GDN_ERR_BAD_SHAPE;
+  *bytes = (size_t)lrec_ws(p, s, op);
+  return GDN_OK;
+}
+
+gdn_status gdn_lrec_saved_size(const gdn_lrec_problem* p, size_t* bytes) {
+  if (!bytes) return GDN_ERR_NULL_POINTER;
+  Lrec s;
+  gdn_status st = check_lrec(p, &s);
+  if (st != GDN_OK) return st;
+  *bytes = (size_t)lrec_chunk_bytes(p, s);
+  return GDN_OK;
+}
+
+gdn_status gdn_lrec_forward(const gdn_lrec_problem* p, const void* x, const void* gate,
+                            const int32_t* lengths, const float* state_in, void* o,
+                            float* state_out, void* saved, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  Lrec s;
+  gdn_status st = check_lrec(p, &s);
+  if (st != GDN_OK) return st;
+  const int64_t need = lrec_ws(p, s, GDN_OP_FORWARD);
+  if (!x || !gate || !o || (need && !workspace)) return GDN_ERR_NULL_POINTER;
+  if (!aligned(x, s.es) || !aligned(gate, s.es) || !aligned(o, s.es) || !aligned(lengths, 4) ||
+      !aligned(state_in, 4) || !aligned(state_out, 4) || !aligned(saved, 16) ||
+      !aligned(workspace, 16))
+    return GDN_ERR_MISALIGNED;
+  if (need && workspace_bytes < (size_t)need) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t n = (int64_t)p->B * p->L * p->C, stb = (int64_t)p->B * p->C * 4;
+  const Region ins[] = {strided(x, p->B, p->L, p->C, p->x_stride, s.es),
+                        strided(gate, p->B, p->L, p->C, p->gate_stride, s.es),
+                        flat(lengths, (int64_t)p->B * 4),
+                        flat(state_out == state_in ? nullptr : state_in, stb)};
+  const Region outs[] = {flat(o, n * s.es), flat(state_out, stb),
+                         flat(saved, lrec_chunk_bytes(p, s)), flat(need ? workspace : nullptr, need)};
+  if (any_meet(outs, 4, ins, 4)) return GDN_ERR_ALIASING;
+  return run_lrec_forward(p, s, x, gate, lengths, state_in, o, state_out, saved, workspace,
+                          static_cast<hipStream_t>(stream));
+}
+
+gdn_status gdn_lrec_step(const gdn_lrec_problem* p, const void* x, const void* gate,
+                         float* state, void* o, void* stream) {
+  if (p && p->L != 1) return GDN_ERR_BAD_SHAPE;
+  if (p && !state) return GDN_ERR_NULL_POINTER;
+  return gdn_lrec_forward(p, x, gate, nullptr, state, o, state, nullptr, nullptr, 0, stream);
+}
+
+gdn_status gdn_lrec_backward(const gdn_lrec_problem* p, const void* x, const void* gate,
+                             const int32_t* lengths, const float* state_in, const void* d_o,
+                             const float* d_state_out, const void* saved, void* dx, void* dgate,
+                             float* d_state_in, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  Lrec s;
+  gdn_status st = check_lrec(p, &s);
+  if (st != GDN_OK) return st;
+  const int64_t need = lrec_ws(p, s, GDN_OP_BACKWARD);
+  if (!x || !gate || !d_o || !dx || !dgate || !workspace) return GDN_ERR_NULL_POINTER;
+  if (!rows_apart(p->B, p->L, p->C, p->dx_stride) ||
+      !rows_apart(p->B, p->L, p->C, p->dgate_stride))
+    return GDN_ERR_BAD_SHAPE;
+  if (!aligned(x, s.es) || !aligned(gate, s.es) || !aligned(d_o, s.es) || !aligned(dx, s.es) ||
+      !aligned(dgate, s.es) || !aligned(lengths, 4) || !aligned(state_in, 4) ||
+      !aligned(d_state_out, 4) || !aligned(d_state_in, 4) || !aligned(saved, 16) ||
+      !aligned(workspace, 16))
+    return GDN_ERR_MISALIGNED;
+  if (workspace_bytes < (size_t)need) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t n = (int64_t)p->B * p->L * p->C, stb = (int64_t)p->B * p->C * 4;
+  const int64_t cb = lrec_chunk_bytes(p, s);
+  const Region ins[] = {strided(x, p->B, p->L, p->C, p->x_stride, s.es),
+                        strided(gate, p->B, p->L, p->C, p->gate_stride, s.es),
+                        flat(lengths, (int64_t)p->B * 4), flat(state_in, stb),
+                        flat(d_o, n * s.es), flat(d_state_out, stb), flat(saved, cb)};
+  const Region outs[] = {strided(dx, p->B, p->L, p->C, p->dx_stride, s.es),
+                         strided(dgate, p->B, p->L, p->C, p->dgate_stride, s.es),
+                         flat(d_state_in, stb), flat(workspace, need)};
+  if (any_meet(outs, 4, ins, 7)) return GDN_ERR_ALIASING;
+  const LrecUse use[] = {{x, p->x_stride},   {gate, p->gate_stride}, {d_o, nullptr},
+                         {dx, p->dx_stride}, {dgate, p->dgate_stride}};
+  const int vec = lrec_vec(p, s.es, 2, use, 5);
+  LrecArgs a{};
+  lrec_args(p, s, vec, &a);
+  a.x = x;
+  a.z = gate;
+  a.len = lengths;
+  a.h0 = state_in;
+  a.d_o = d_o;
+  a.dhT = d_state_out;
+  a.dx = dx;
+  a.dz = dgate;
+  a.dx_sb = p->dx_stride[0];
+  a.dx_sl = p->dx_stride[1];
+  a.dz_sb = p->dgate_stride[0];
+  a.dz_sl = p->dgate_stride[1];
+  a.dh0 = d_state_in;
+  char* ws = static_cast<char*>(workspace);
+  a.compA = reinterpret_cast<float*>(ws);
+  a.compH = reinterpret_cast<float*>(ws + cb);
+  a.enter = saved ? const_cast<float*>(static_cast<const float*>(saved))
+                  : reinterpret_cast<float*>(ws + 2 * cb);
+  return hip_status(
+      launch_lrec_backward(a, s.io, vec, saved != nullptr, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,96 @@
+// Kernel argument blocks and launchers of the block's operators, shared
+// between their kernels and the host side (gdn_block_api.hip).  Not part of
+// the public interface.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_device.h"
+
+namespace gdn {
+
+// Head dims up to this; half as many pairs.
+constexpr int kRowMaxD = 256;
+
+// A [B, L, H, D] tensor by its batch and token strides (elements).
+struct RowView {
+  const void* p;
+  int64_t sb, sl;
+};
+
+// How a row of D values lies over lanes: every lane holds two pieces of V
+// elements, so that both members of a rotated pair are in one lane.  `lanes`
+// lanes hold a row, `group` (the power of two from there) are given to it;
+// a wave holds 64 / group rows.
+struct RowShape {
+  int D, lanes, group;
+  int V;
+};
+
+struct PackArgs {
+  RowView x;
+  void* v;         // [B, L, H, D] uint8
+  void* scale;     // [B, L, H] uint8
+  int B, L, H;
+  RowShape row;
+};
+
+struct QkArgs {
+  RowView x[2];            // q, k (backward: dq, dk go to dx)
+  const uint8_t* v8[2];    // checkpoints read in place of x
+  const uint8_t* s8[2];
+  const float* w[2];       // fp32 [D] or nullptr
+  const int32_t* pos;      // [B or 1, L, axes]
+  const int32_t* len;      // [B] or nullptr
+  void* y[2];              // forward: out; backward: the incoming gradient
+  uint8_t* v8_out[2];      // forward: checkpoints written, or nullptr
+  uint8_t* s8_out[2];
+  RowView dx[2];           // backward: gradients
+  float* part;             // backward: per-workgroup weight gradients [wgs][2][D]
+  float* dw[2];
+  int B, L, H[2];
+  RowShape row;
+  int norm, adjacent, axes, pairs, bound1, bound2;   // pairs of axes 0, of 0 and 1
+  int pos_shared;
+  float eps, c;
+  // turns (angle / 2 pi) per unit of position of every pair
+  double turns[kRowMaxD / 2];
+};
+
+struct LrecArgs {
+  const void* x;
+  const void* z;
+  int64_t x_sb, x_sl, z_sb, z_sl;
+  const int32_t* len;
+  const float* h0;       // [B, C] or nullptr
+  void* o;               // [B, L, C]
+  float* hT;             // [B, C] or nullptr
+  float* enter;          // [B, chunks, C] state entering every chunk
+  const void* d_o;
+  const float* dhT;
+  void* dx;
+  void* dz;
+  int64_t dx_sb, dx_sl, dz_sb, dz_sl;
+  float* dh0;
+  float* compA;          // [B, chunks, C]
+  float* compH;
+  int B, L, C, chunks, strips;
+  int logits, complement;
+};
+
+// Tokens of a chunk of the recurrence.
+constexpr int kLrecChunk = 128;
+
+hipError_t launch_pack8(const PackArgs& a, int io, hipStream_t s);
+hipError_t launch_unpack8(const PackArgs& a, int io, hipStream_t s);
+hipError_t launch_qk_forward(const QkArgs& a, int io, bool packed, hipStream_t s);
+// Workgroups of the backward pass: rows of `part`.
+int qk_backward_wgs(int64_t tokens);
+hipError_t launch_qk_backward(const QkArgs& a, int io, bool packed, hipStream_t s);
+// vec: elements a lane takes of a row at once (1, 2 or 4)
+hipError_t launch_lrec_forward(const LrecArgs& a, int io, int vec, hipStream_t s);
+hipError_t launch_lrec_backward(const LrecArgs& a, int io, int vec, bool have_enter,
+                                hipStream_t s);
+
+}  // namespace gdn

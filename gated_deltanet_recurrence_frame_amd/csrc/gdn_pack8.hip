@@ -1,0 +1,123 @@
+// 8-bit checkpoints of activation rows (gdn_pack8, gdn_unpack8).
+//
+// A row x of D values is kept as e4m3(x 2^(127 - s)) and its byte s.  The
+// scale is a power of two, so scaling is exact and the only rounding is the
+// conversion's.  Bytes alone bound both passes: 3 D + 1 a bf16 row.
+#include "gdn_rows.h"
+
+namespace gdn {
+
+constexpr int kPackThreads = 256;
+constexpr int kPackWaves = kPackThreads / 64;
+constexpr int kPackRows = 4;    // rows of a lane in flight
+
+template <int IO, int V>
+__global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
+  const int rpw = 64 / a.row.group;
+  const uint32_t rows = (uint32_t)a.B * a.L * a.H;
+  const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
+  const bool in_row = j < a.row.lanes;
+  const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
+  float f[kPackRows][2 * V];
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const uint32_t r = base + i * rpw;
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) f[i][e] = 0.f;
+    if (in_row && r < rows) {
+      const uint32_t tok = r / (uint32_t)a.H, h = r - tok * (uint32_t)a.H;
+      const uint32_t b = tok / (uint32_t)a.L, l = tok - b * (uint32_t)a.L;
+      const char* p = static_cast<const char*>(a.x.p) +
+                      ((int64_t)b * a.x.sb + (int64_t)l * a.x.sl + (int64_t)h * a.row.D +
+                       2 * j * V) * Io<IO>::bytes;
+      row_load<IO, V>(p, f[i]);
+      row_load<IO, V>(p + V * Io<IO>::bytes, f[i] + V);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const uint32_t r = base + i * rpw;
+    const int s = scale_byte(group_max(finite_max<2 * V>(f[i]), a.row.group));
+    const float m = pack_factor(s);
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) f[i][e] *= m;
+    if (r < rows) {
+      if (in_row) {
+        uint8_t* v = static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D + 2 * j * V;
+        e4m3_store<V>(v, f[i]);
+        e4m3_store<V>(v + V, f[i] + V);
+      }
+      if (j == 0) static_cast<uint8_t*>(a.scale)[r] = (uint8_t)s;
+    }
+  }
+}
+
+template <int IO, int V>
+__global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
+  const int rpw = 64 / a.row.group;
+  const uint32_t rows = (uint32_t)a.B * a.L * a.H;
+  const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
+  const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
+  if (j >= a.row.lanes) return;
+  float f[kPackRows][2 * V];
+  float m[kPackRows];
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const uint32_t r = base + i * rpw;
+    if (r < rows) {
+      const uint8_t* v = static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D + 2 * j * V;
+      e4m3_load<V>(v, f[i]);
+      e4m3_load<V>(v + V, f[i] + V);
+      m[i] = unpack_factor(static_cast<const uint8_t*>(a.scale)[r]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const uint32_t r = base + i * rpw;
+    if (r < rows) {
+#pragma unroll
+      for (int e = 0; e < 2 * V; ++e) f[i][e] *= m[i];
+      const uint32_t tok = r / (uint32_t)a.H, h = r - tok * (uint32_t)a.H;
+      const uint32_t b = tok / (uint32_t)a.L, l = tok - b * (uint32_t)a.L;
+      char* p = const_cast<char*>(static_cast<const char*>(a.x.p)) +
+                ((int64_t)b * a.x.sb + (int64_t)l * a.x.sl + (int64_t)h * a.row.D + 2 * j * V) *
+                    Io<IO>::bytes;
+      row_store<IO, V>(p, f[i]);
+      row_store<IO, V>(p + V * Io<IO>::bytes, f[i] + V);
+    }
+  }
+}
+
+static unsigned pack_grid(const PackArgs& a) {
+  const int64_t rows = (int64_t)a.B * a.L * a.H;
+  const int64_t per = (int64_t)kPackWaves * (64 / a.row.group) * kPackRows;
+  return (unsigned)((rows + per - 1) / per);
+}
+
+hipError_t launch_pack8(const PackArgs& a, int io, hipStream_t s) {
+  const dim3 g(pack_grid(a)), t(kPackThreads);
+  if (io == IO_BF16) {
+    if (a.row.V == 8) hipLaunchKernelGGL((pack8_kernel<IO_BF16, 8>), g, t, 0, s, a);
+    else if (a.row.V == 4) hipLaunchKernelGGL((pack8_kernel<IO_BF16, 4>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((pack8_kernel<IO_BF16, 2>), g, t, 0, s, a);
+  } else {
+    if (a.row.V == 4) hipLaunchKernelGGL((pack8_kernel<IO_F32, 4>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((pack8_kernel<IO_F32, 2>), g, t, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_unpack8(const PackArgs& a, int io, hipStream_t s) {
+  const dim3 g(pack_grid(a)), t(kPackThreads);
+  if (io == IO_BF16) {
+    if (a.row.V == 8) hipLaunchKernelGGL((unpack8_kernel<IO_BF16, 8>), g, t, 0, s, a);
+    else if (a.row.V == 4) hipLaunchKernelGGL((unpack8_kernel<IO_BF16, 4>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((unpack8_kernel<IO_BF16, 2>), g, t, 0, s, a);
+  } else {
+    if (a.row.V == 4) hipLaunchKernelGGL((unpack8_kernel<IO_F32, 4>), g, t, 0, s, a);
+    else hipLaunchKernelGGL((unpack8_kernel<IO_F32, 2>), g, t, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -1,0 +1,191 @@
+/*
+ * libgdn: operators of the block around the token mixer (gdn.h), for MI355X
+ * (gfx950).
+ *
+ *   qk      queries and keys of a projection, normalised per head and rotated
+ *           by position in one pass (what gdn_forward's q and k are made by),
+ *           and the gradient of that;
+ *   pack8   8-bit checkpoints of activation rows, kept from the forward to
+ *           the backward pass in place of the rows: written by the qk forward
+ *           in its own pass, read by the qk backward (and by a recomputing qk
+ *           forward), or packed and unpacked by themselves;
+ *   lrec    a gated linear recurrence over the tokens, one state per channel
+ *           (the D x D recurrence's cheap companion): whole sequence, one
+ *           token at a time, and backward.
+ *
+ * Conventions are gdn.h's (device pointers owned by the caller, work enqueued
+ * on `stream`, nothing synchronises, host-side validation before any launch,
+ * gdn_status results, capture into HIP graphs), with these differences:
+ *   - Inputs that a block takes out of one projection may be strided views:
+ *     element (b, l, h, d) of q at q[b stride[0] + l stride[1] + h D + d],
+ *     strides in elements.  Strides of inputs are >= 0 (0 repeats a row);
+ *     rows of an output must not overlap each other.  Two outputs, or an
+ *     output and an input, may be interleaved views of one allocation.
+ *   - io pointers need the alignment of two elements for qk and pack8 (4
+ *     bytes for bf16, 8 for fp32) and of one element for lrec, fp32 and
+ *     int32 pointers 4 bytes, workspaces and saved buffers 16; strides of qk
+ *     and pack8 are even.  Rows that are 16-byte aligned are the fast case.
+ *   - Sizes are at least 1; B * L at most 2^31 - 1, at most 2^40 elements a
+ *     tensor, strides at most 2^40.
+ *   - `lengths` is NULL or B device int32s, the number of tokens of each
+ *     sequence of a padded batch (values outside 0 .. L count as 0 or L).
+ *     What the inputs hold behind a sequence's last token is never read; the
+ *     outputs there are written as zeros.
+ */
+#ifndef LIBGDN_GDN_BLOCK_H
+#define LIBGDN_GDN_BLOCK_H
+
+#include "gdn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- 8-bit checkpoints -------------------------------------------------
+ * A row (one token's one head, D values x) is kept as D bytes v and one byte
+ * s: x ~ e4m3(v) 2^(s - 127).  s is the smallest that keeps the row's
+ * largest finite |x| within 448, e4m3's largest value (s = 0 for a row of
+ * zeros, and at the type's lower end); v is x 2^(127 - s), exact as a power
+ * of two scales it, rounded to the nearest e4m3 (ties to even): relative
+ * error at most 2^-4 down to 2^-14 of the row's largest value.  Infinities
+ * and NaN become NaN (0x7f or 0xff) and do not count for s. */
+typedef struct {
+    void* values;           /* [B, L, H, D] uint8, contiguous */
+    void* scale;            /* [B, L, H]    uint8, contiguous */
+} gdn_checkpoint;
+
+typedef struct {
+    int32_t B, L, H, D;     /* D a multiple of 4, at most 256 */
+    int32_t io_dtype;       /* gdn_dtype of x */
+    int32_t reserved;       /* 0 */
+    int64_t stride[2];      /* of x: batches, tokens */
+} gdn_pack8_problem;
+
+/* Checkpoint of x [B, L, H, D] (strided). */
+gdn_status gdn_pack8(const gdn_pack8_problem* p, const void* x, const gdn_checkpoint* to,
+                     void* stream);
+
+/* x [B, L, H, D] (strided) of a checkpoint, rounded once to the io type (bf16
+ * holds e4m3's four significant bits exactly).  Rows overlapping each other
+ * are GDN_ERR_BAD_SHAPE. */
+gdn_status gdn_unpack8(const gdn_pack8_problem* p, const gdn_checkpoint* from, void* x,
+                       void* stream);
+
+/* ---- queries and keys: norm and rotation -------------------------------
+ * For every row x (D values) of q [B, L, Hq, D] and k [B, L, Hk, D]:
+ *   r  = 1 / sqrt(c |x|^2 + eps), c = 1 (L2) or 1 / D (RMS); 0 where the
+ *        argument is 0; 1 without a norm;
+ *   n  = r x w, w the operand's fp32 weights [D] or 1;
+ *   y  = n with its first 2 P values turned in pairs, P = sum of axis_pairs:
+ *        y_i = n_i cos phi - n_j sin phi, y_j = n_i sin phi + n_j cos phi,
+ *        (i, j) = (m, m + P) (halves) or (2m, 2m + 1) (adjacent), m < P;
+ *        pair m is the f-th of its axis a's n_a pairs and
+ *        phi = positions[b, l, a] theta^(-f / n_a), formed in 64 bits.
+ * Sums are fp32, y is rounded once to the io type.  The sum of squares is
+ * formed as it stands: rows beyond 1e19 or, without eps, below 1e-19 in
+ * magnitude over- or underflow it. */
+typedef enum { GDN_NORM_NONE = 0, GDN_NORM_L2 = 1, GDN_NORM_RMS = 2 } gdn_qk_norm;
+typedef enum { GDN_PAIR_HALVES = 0, GDN_PAIR_ADJACENT = 1 } gdn_qk_pairing;
+
+typedef struct {
+    int32_t B, L, Hq, Hk, D;    /* D a multiple of 4, at most 256 */
+    int32_t io_dtype;           /* gdn_dtype of q, k and their gradients */
+    int32_t norm;               /* gdn_qk_norm */
+    int32_t pairing;            /* gdn_qk_pairing */
+    int32_t axes;               /* coordinates of a position, 0 (no rotation) .. 3 */
+    int32_t axis_pairs[3];      /* pairs of each axis; P even, 2 P <= D */
+    int32_t shared_positions;   /* 1: one [L, axes] table for all batches */
+    float eps;                  /* >= 0 */
+    double theta;               /* > 0 */
+    int64_t q_stride[2], k_stride[2];     /* of q, k: batches, tokens */
+    int64_t dq_stride[2], dk_stride[2];   /* of dq, dk (backward) */
+} gdn_qk_problem;
+
+/* y of q and k.
+ *   q, k       the rows, or NULL with `from` set.
+ *   from       NULL, or two checkpoints (of q, of k) read in place of q, k:
+ *              recomputation in a backward pass.
+ *   positions  int32 [B, L, axes] (or [L, axes]), NULL when axes is 0.
+ *   q_weight, k_weight  fp32 [D] or NULL; only with a norm.
+ *   q_out, k_out  [B, L, Hq, D], [B, L, Hk, D] contiguous: gdn_forward's q, k.
+ *   to         NULL, or two checkpoints (of q, of k) that receive the raw
+ *              rows; not together with `from`. */
+gdn_status gdn_qk_forward(const gdn_qk_problem* p, const void* q, const void* k,
+                          const gdn_checkpoint* from, const float* q_weight,
+                          const float* k_weight, const int32_t* positions,
+                          const int32_t* lengths, void* q_out, void* k_out,
+                          const gdn_checkpoint* to, void* stream);
+
+/* Bytes of workspace of gdn_qk_backward; 0 when want_weights is 0. */
+gdn_status gdn_qk_workspace_size(const gdn_qk_problem* p, int want_weights, size_t* bytes);
+
+/* Gradients.  With g = (dy turned by -phi):
+ *   dw = sum over rows of g r x;  dx = r (g w - x r^2 c sum(x g w)) (0 for a
+ *   zero row without eps; g w without a norm).
+ *   q, k / from   as the forward's; neither is needed (NULL) without a norm.
+ *   d_qout, d_kout  contiguous, io type.
+ *   dq, dk        io type, strided.
+ *   dq_weight, dk_weight  fp32 [D], both or neither; with a norm only.
+ *                 Summed in a fixed order. */
+gdn_status gdn_qk_backward(const gdn_qk_problem* p, const void* q, const void* k,
+                           const gdn_checkpoint* from, const float* q_weight,
+                           const float* k_weight, const int32_t* positions,
+                           const int32_t* lengths, const void* d_qout, const void* d_kout,
+                           void* dq, void* dk, float* dq_weight, float* dk_weight,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- gated linear recurrence -------------------------------------------
+ * For every batch and channel, over the tokens l = 1 .. L:
+ *   h_l = a_l h_{l-1} + u_l,  o_l = h_l,
+ *   a   = gate, or sigmoid(gate) with GDN_FLAG_GATE_LOGITS,
+ *   u   = x, or (1 - a) x with GDN_LREC_COMPLEMENT.
+ * A gate of exactly 0 (a logit of -inf) starts the state anew.  The state
+ * and both scans are fp32; o is rounded once to the io type. */
+enum { GDN_LREC_COMPLEMENT = 4 };   /* a bit beside gdn_flag's */
+
+typedef struct {
+    int32_t B, L, C;
+    int32_t io_dtype;           /* gdn_dtype of x, gate, o and their gradients */
+    int32_t flags;              /* GDN_FLAG_GATE_LOGITS | GDN_LREC_COMPLEMENT */
+    int32_t reserved;           /* 0 */
+    int64_t x_stride[2], gate_stride[2];     /* of x, gate: batches, tokens */
+    int64_t dx_stride[2], dgate_stride[2];   /* of dx, dgate (backward) */
+} gdn_lrec_problem;
+
+/* Bytes of workspace of gdn_lrec_forward / _step / _backward (op: gdn_op). */
+gdn_status gdn_lrec_workspace_size(const gdn_lrec_problem* p, int op, size_t* bytes);
+
+/* Bytes of the optional forward->backward buffer: the state entering every
+ * chunk of tokens, fp32 (under 1% of x). */
+gdn_status gdn_lrec_saved_size(const gdn_lrec_problem* p, size_t* bytes);
+
+/* Whole sequence.  o [B, L, C] contiguous; state_in, state_out fp32 [B, C];
+ * state_in NULL is zero, state_out NULL is not written and may be state_in;
+ * saved NULL or gdn_lrec_saved_size bytes.  state_out is the state after the
+ * sequence's last token (state_in for a length of 0). */
+gdn_status gdn_lrec_forward(const gdn_lrec_problem* p, const void* x, const void* gate,
+                            const int32_t* lengths, const float* state_in, void* o,
+                            float* state_out, void* saved, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* One token (p->L must be 1), the state [B, C] carried in place. */
+gdn_status gdn_lrec_step(const gdn_lrec_problem* p, const void* x, const void* gate,
+                         float* state, void* o, void* stream);
+
+/* Gradients.  G_l = do_l + a_{l+1} G_{l+1} (G_L also + d_state_out):
+ *   dx = G or (1 - a) G,  da = G (h_{l-1} [- x]),  dgate = da or da a (1 - a),
+ *   d_state_in = a_1 G_1.
+ *   d_o       [B, L, C] contiguous, io type.
+ *   saved     the forward's buffer, or NULL to form it again.
+ *   d_state_out NULL is zero; d_state_in NULL is not written. */
+gdn_status gdn_lrec_backward(const gdn_lrec_problem* p, const void* x, const void* gate,
+                             const int32_t* lengths, const float* state_in, const void* d_o,
+                             const float* d_state_out, const void* saved, void* dx, void* dgate,
+                             float* d_state_in, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LIBGDN_GDN_BLOCK_H */

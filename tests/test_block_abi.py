@@ -1,0 +1,373 @@
+"""CPU checks of the block's entry points (include/gdn_block.h): exports,
+sizes, and host-side validation; every call here fails validation before any
+GPU work (the addresses are never dereferenced)."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from gated_deltanet_recurrence_frame_amd import binding as gb
+from gated_deltanet_recurrence_frame_amd import block
+
+VP = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(gb.LIB_PATH):
+        pytest.fail("libgdn.so is not built; run __graft_entry__.build()")
+    return block.lib()
+
+
+def name(code):
+    return gb.STATUS[code]
+
+
+def at(i, off=0):
+    """Fake addresses far apart."""
+    return VP((i + 1) * (1 << 40) + off)
+
+
+def test_exports_every_declared_function(lib):
+    with open(block.HEADER) as f:
+        names = set(re.findall(r"^gdn_status\s+(gdn_\w+)\s*\(", f.read(), re.M))
+    assert names == {"gdn_pack8", "gdn_unpack8", "gdn_qk_forward", "gdn_qk_workspace_size",
+                     "gdn_qk_backward", "gdn_lrec_workspace_size", "gdn_lrec_saved_size",
+                     "gdn_lrec_forward", "gdn_lrec_step", "gdn_lrec_backward"}
+    for n in names:
+        assert getattr(lib, n).argtypes, n
+
+
+def ckpt(i):
+    return (block.GdnCheckpoint * 2)(block.GdnCheckpoint(at(i), at(i + 1)),
+                                     block.GdnCheckpoint(at(i + 2), at(i + 3)))
+
+
+# ---- pack8 ----
+
+def pack(lib, over=None, x=at(0), values=at(1), scale=at(2), unpack=False):
+    p = block._pack8_problem((2, 3, 4, 112), "bf16", (3 * 448, 448))
+    for k, v in (over or {}).items():
+        if k == "stride":
+            p.stride[0], p.stride[1] = v
+        else:
+            setattr(p, k, v)
+    c = block.GdnCheckpoint(values, scale)
+    if unpack:
+        return name(lib.gdn_unpack8(ctypes.byref(p), ctypes.byref(c), x, None))
+    return name(lib.gdn_pack8(ctypes.byref(p), x, ctypes.byref(c), None))
+
+
+@pytest.mark.parametrize("over,status", [
+    ({"B": 0}, "GDN_ERR_BAD_SHAPE"), ({"L": -1}, "GDN_ERR_BAD_SHAPE"),
+    ({"H": 0}, "GDN_ERR_BAD_SHAPE"), ({"D": 0}, "GDN_ERR_BAD_SHAPE"),
+    ({"D": 6}, "GDN_ERR_UNSUPPORTED"), ({"D": 260}, "GDN_ERR_UNSUPPORTED"),
+    ({"reserved": 1}, "GDN_ERR_UNSUPPORTED"), ({"io_dtype": 2}, "GDN_ERR_BAD_DTYPE"),
+    ({"B": 1 << 20, "L": 1 << 12}, "GDN_ERR_BAD_SHAPE"),
+    ({"stride": (-8, 448)}, "GDN_ERR_BAD_SHAPE"),
+    ({"stride": (1 << 41, 448)}, "GDN_ERR_BAD_SHAPE"),
+    ({"B": 9, "stride": (1 << 40, 448)}, "GDN_ERR_BAD_SHAPE"),
+    ({"stride": (4 * 448, 449)}, "GDN_ERR_MISALIGNED"),
+])
+def test_pack8_refusals(lib, over, status):
+    assert pack(lib, over) == status
+    assert pack(lib, over, unpack=True) == status
+
+
+def test_pack8_pointers(lib):
+    assert pack(lib, x=None) == "GDN_ERR_NULL_POINTER"
+    assert pack(lib, values=None) == "GDN_ERR_NULL_POINTER"
+    assert pack(lib, scale=None, unpack=True) == "GDN_ERR_NULL_POINTER"
+    assert name(lib.gdn_pack8(None, at(0), None, None)) == "GDN_ERR_NULL_POINTER"
+    assert pack(lib, x=at(0, 2)) == "GDN_ERR_MISALIGNED"
+    assert pack(lib, values=at(1, 1)) == "GDN_ERR_MISALIGNED"
+    assert pack(lib, values=at(0, 64)) == "GDN_ERR_ALIASING"
+    assert pack(lib, scale=at(0, 64)) == "GDN_ERR_ALIASING"
+    assert pack(lib, scale=at(1, 64)) == "GDN_ERR_ALIASING"
+    # rows of the unpacked tensor over each other
+    assert pack(lib, {"stride": (448, 448)}, unpack=True) == "GDN_ERR_BAD_SHAPE"
+    assert pack(lib, {"stride": (3 * 448, 440)}, unpack=True) == "GDN_ERR_BAD_SHAPE"
+
+
+# ---- qk ----
+
+def qk_problem(**over):
+    p = block.make_qk_problem(2, 5, 4, 2, 64, "bf16", "rms", 1e-6, (32,), "halves", 1e4)
+    for k, v in over.items():
+        if k == "axis_pairs":
+            for i in range(3):
+                p.axis_pairs[i] = v[i]
+        elif k.endswith("stride"):
+            getattr(p, k)[0], getattr(p, k)[1] = v
+        else:
+            setattr(p, k, v)
+    return p
+
+
+def qk_forward(lib, p, q=at(0), k=at(1), src=None, wq=at(2), wk=at(3), pos=at(4), n=None,
+               qo=at(5), ko=at(6), to=None):
+    return name(lib.gdn_qk_forward(ctypes.byref(p) if p is not None else None, q, k, src, wq, wk,
+                                   pos, n, qo, ko, to, None))
+
+
+def qk_backward(lib, p, q=at(0), k=at(1), src=None, wq=at(2), wk=at(3), pos=at(4), n=None,
+                gq=at(5), gk=at(6), dq=at(7), dk=at(8), dwq=at(9), dwk=at(10), ws=at(11),
+                nws=1 << 20):
+    return name(lib.gdn_qk_backward(ctypes.byref(p), q, k, src, wq, wk, pos, n, gq, gk, dq, dk,
+                                    dwq, dwk, ws, nws, None))
+
+
+@pytest.mark.parametrize("over,status", [
+    ({"B": 0}, "GDN_ERR_BAD_SHAPE"), ({"L": 0}, "GDN_ERR_BAD_SHAPE"),
+    ({"Hq": 0}, "GDN_ERR_BAD_SHAPE"), ({"Hk": -1}, "GDN_ERR_BAD_SHAPE"),
+    ({"D": 66}, "GDN_ERR_UNSUPPORTED"), ({"D": 260}, "GDN_ERR_UNSUPPORTED"),
+    ({"io_dtype": 7}, "GDN_ERR_BAD_DTYPE"), ({"norm": 3}, "GDN_ERR_UNSUPPORTED"),
+    ({"pairing": 2}, "GDN_ERR_UNSUPPORTED"), ({"shared_positions": 2}, "GDN_ERR_UNSUPPORTED"),
+    ({"axes": 4}, "GDN_ERR_BAD_SHAPE"), ({"axes": 0}, "GDN_ERR_BAD_SHAPE"),
+    ({"axes": 2}, "GDN_ERR_BAD_SHAPE"),                       # the second axis has no pairs
+    ({"axis_pairs": (34, 0, 0)}, "GDN_ERR_BAD_SHAPE"),        # more than the head holds
+    ({"axis_pairs": (31, 0, 0)}, "GDN_ERR_BAD_SHAPE"),        # odd
+    ({"axis_pairs": (-2, 0, 0)}, "GDN_ERR_BAD_SHAPE"),
+    ({"theta": 0.0}, "GDN_ERR_BAD_SHAPE"), ({"theta": float("nan")}, "GDN_ERR_BAD_SHAPE"),
+    ({"eps": -1.0}, "GDN_ERR_BAD_SHAPE"), ({"eps": float("inf")}, "GDN_ERR_BAD_SHAPE"),
+    ({"B": 1 << 16, "L": 1 << 14}, "GDN_ERR_BAD_SHAPE"),
+    ({"q_stride": (-2, 256)}, "GDN_ERR_BAD_SHAPE"),
+    ({"dk_stride": (1 << 41, 256)}, "GDN_ERR_BAD_SHAPE"),
+])
+def test_qk_refusals(lib, over, status):
+    p = qk_problem(**over)
+    assert qk_forward(lib, p) == status
+    assert qk_backward(lib, p) == status
+    n = ctypes.c_size_t(0)
+    assert name(lib.gdn_qk_workspace_size(ctypes.byref(p), 1, ctypes.byref(n))) == status
+
+
+def test_qk_pointers(lib):
+    p = qk_problem()
+    assert qk_forward(lib, None) == "GDN_ERR_NULL_POINTER"
+    for arg in ("q", "k", "pos", "qo", "ko"):
+        assert qk_forward(lib, p, **{arg: None}) == "GDN_ERR_NULL_POINTER", arg
+    for arg in ("q", "k", "pos", "gq", "gk", "dq", "dk", "dwq", "dwk", "ws"):
+        assert qk_backward(lib, p, **{arg: None}) == "GDN_ERR_NULL_POINTER", arg
+    assert qk_forward(lib, p, src=ckpt(20)) == "GDN_ERR_NULL_POINTER"      # rows and checkpoints
+    half = ckpt(20)
+    half[1].scale = None
+    assert qk_forward(lib, p, q=None, k=None, src=half) == "GDN_ERR_NULL_POINTER"
+    assert qk_forward(lib, p, to=half) == "GDN_ERR_NULL_POINTER"
+    assert qk_forward(lib, p, q=None, k=None, src=ckpt(20), to=ckpt(30)) == "GDN_ERR_UNSUPPORTED"
+    assert qk_forward(lib, qk_problem(norm=0)) == "GDN_ERR_UNSUPPORTED"    # weights, no norm
+    assert qk_backward(lib, qk_problem(norm=0), wq=None, wk=None) == "GDN_ERR_UNSUPPORTED"
+    assert qk_backward(lib, p, nws=16) == "GDN_ERR_WORKSPACE_TOO_SMALL"
+    for arg, off in (("q", 2), ("qo", 2), ("wq", 2), ("pos", 1), ("n", 2)):
+        assert qk_forward(lib, p, **{arg: at(50, off)}) == "GDN_ERR_MISALIGNED", arg
+    for arg, off in (("dq", 2), ("gk", 2), ("dwq", 2), ("ws", 8)):
+        assert qk_backward(lib, p, **{arg: at(50, off)}) == "GDN_ERR_MISALIGNED", arg
+    assert qk_forward(lib, qk_problem(q_stride=(1280, 257))) == "GDN_ERR_MISALIGNED"
+
+
+def test_qk_aliasing(lib):
+    p = qk_problem()
+    assert qk_forward(lib, p, qo=at(0)) == "GDN_ERR_ALIASING"              # in place
+    assert qk_forward(lib, p, ko=at(5, 64)) == "GDN_ERR_ALIASING"
+    assert qk_forward(lib, p, qo=at(4)) == "GDN_ERR_ALIASING"
+    to = ckpt(20)
+    to[0].scale = at(5)
+    assert qk_forward(lib, p, to=to) == "GDN_ERR_ALIASING"
+    assert qk_backward(lib, p, dq=at(5)) == "GDN_ERR_ALIASING"
+    assert qk_backward(lib, p, ws=at(0)) == "GDN_ERR_ALIASING"
+    assert qk_backward(lib, p, dwk=at(9)) == "GDN_ERR_ALIASING"
+    # rows of one gradient over each other
+    assert qk_backward(lib, qk_problem(dq_stride=(1280, 128))) == "GDN_ERR_BAD_SHAPE"
+    assert qk_backward(lib, qk_problem(dk_stride=(128, 128))) == "GDN_ERR_BAD_SHAPE"
+    # views of one projection: [B, L, 8 heads, 64], q 4 heads, k 2; the
+    # gradients interleave without meeting (nothing is wrong but the
+    # workspace), or overlap by one head
+    s = (5 * 512, 512)
+    p = qk_problem(q_stride=s, k_stride=s, dq_stride=s, dk_stride=s)
+    view = dict(q=at(0), k=at(0, 512), dq=at(7), dk=at(7, 512), nws=16)
+    assert qk_backward(lib, p, **view) == "GDN_ERR_WORKSPACE_TOO_SMALL"
+    view = dict(q=at(0), k=at(0, 512), dq=at(7), dk=at(7, 384))
+    assert qk_backward(lib, p, **view) == "GDN_ERR_ALIASING"
+    # the gradient over its own projection
+    view = dict(q=at(0), k=at(0, 512), dq=at(0, 768), dk=at(7))
+    assert qk_backward(lib, p, **view) == "GDN_ERR_ALIASING"
+
+
+def test_qk_workspace_size(lib):
+    assert block.qk_workspace_size(qk_problem(), False) == 0
+    n = block.qk_workspace_size(qk_problem(), True)
+    assert n > 0 and n % (2 * 64 * 4) == 0
+    big = block.make_qk_problem(1, 106480, 20, 20, 112)
+    assert n <= block.qk_workspace_size(big, True) <= 1 << 22
+
+
+# ---- lrec ----
+
+def lrec_problem(**over):
+    p = block.make_lrec_problem(2, 300, 24, "bf16", True, True)
+    for k, v in over.items():
+        if k.endswith("stride"):
+            getattr(p, k)[0], getattr(p, k)[1] = v
+        else:
+            setattr(p, k, v)
+    return p
+
+
+def lrec_forward(lib, p, x=at(0), z=at(1), n=at(2), h0=at(3), o=at(4), hT=at(5), saved=at(6),
+                 ws=at(7), nws=1 << 24):
+    return name(lib.gdn_lrec_forward(ctypes.byref(p) if p is not None else None, x, z, n, h0, o,
+                                     hT, saved, ws, nws, None))
+
+
+def lrec_backward(lib, p, x=at(0), z=at(1), n=at(2), h0=at(3), d=at(4), dh=at(5), saved=at(6),
+                  dx=at(7), dz=at(8), dh0=at(9), ws=at(10), nws=1 << 24):
+    return name(lib.gdn_lrec_backward(ctypes.byref(p), x, z, n, h0, d, dh, saved, dx, dz, dh0, ws,
+                                      nws, None))
+
+
+@pytest.mark.parametrize("over,status", [
+    ({"B": 0}, "GDN_ERR_BAD_SHAPE"), ({"L": 0}, "GDN_ERR_BAD_SHAPE"),
+    ({"C": -3}, "GDN_ERR_BAD_SHAPE"), ({"io_dtype": 2}, "GDN_ERR_BAD_DTYPE"),
+    ({"flags": 1}, "GDN_ERR_UNSUPPORTED"), ({"flags": 8}, "GDN_ERR_UNSUPPORTED"),
+    ({"reserved": 1}, "GDN_ERR_UNSUPPORTED"),
+    ({"L": (1 << 31) - 1}, "GDN_ERR_BAD_SHAPE"), ({"C": (1 << 31) - 1}, "GDN_ERR_BAD_SHAPE"),
+    ({"B": 1 << 16, "L": 1 << 14, "C": 1 << 11}, "GDN_ERR_BAD_SHAPE"),
+    ({"x_stride": (-1, 24)}, "GDN_ERR_BAD_SHAPE"),
+    ({"dgate_stride": (24, 1 << 41)}, "GDN_ERR_BAD_SHAPE"),
+])
+def test_lrec_refusals(lib, over, status):
+    p = lrec_problem(**over)
+    assert lrec_forward(lib, p) == status
+    assert lrec_backward(lib, p) == status
+    n = ctypes.c_size_t(0)
+    assert name(lib.gdn_lrec_workspace_size(ctypes.byref(p), 0, ctypes.byref(n))) == status
+    assert name(lib.gdn_lrec_saved_size(ctypes.byref(p), ctypes.byref(n))) == status
+
+
+def test_lrec_pointers(lib):
+    p = lrec_problem()
+    assert lrec_forward(lib, None) == "GDN_ERR_NULL_POINTER"
+    for arg in ("x", "z", "o", "ws"):
+        assert lrec_forward(lib, p, **{arg: None}) == "GDN_ERR_NULL_POINTER", arg
+    for arg in ("x", "z", "d", "dx", "dz", "ws"):
+        assert lrec_backward(lib, p, **{arg: None}) == "GDN_ERR_NULL_POINTER", arg
+    assert lrec_forward(lib, p, nws=16) == "GDN_ERR_WORKSPACE_TOO_SMALL"
+    assert lrec_backward(lib, p, nws=16) == "GDN_ERR_WORKSPACE_TOO_SMALL"
+    for arg, off in (("x", 1), ("o", 1), ("h0", 2), ("n", 2), ("saved", 8), ("ws", 4)):
+        assert lrec_forward(lib, p, **{arg: at(50, off)}) == "GDN_ERR_MISALIGNED", arg
+    for arg, off in (("d", 1), ("dx", 1), ("dh", 2), ("dh0", 2), ("ws", 4)):
+        assert lrec_backward(lib, p, **{arg: at(50, off)}) == "GDN_ERR_MISALIGNED", arg
+    for arg in ("o", "hT", "saved", "ws"):
+        assert lrec_forward(lib, p, **{arg: at(1)}) == "GDN_ERR_ALIASING", arg
+    assert lrec_forward(lib, p, hT=at(3, 4)) == "GDN_ERR_ALIASING"         # part of state_in
+    assert lrec_forward(lib, p, hT=at(3), nws=0) == "GDN_ERR_WORKSPACE_TOO_SMALL"   # in place
+    for arg in ("dx", "dz", "dh0", "ws"):
+        assert lrec_backward(lib, p, **{arg: at(4)}) == "GDN_ERR_ALIASING", arg
+    assert lrec_backward(lib, p, dz=at(7)) == "GDN_ERR_ALIASING"
+    assert lrec_backward(lib, lrec_problem(dx_stride=(24, 24))) == "GDN_ERR_BAD_SHAPE"
+    # the two gradients as halves of one tensor
+    s = (300 * 48, 48)
+    p = lrec_problem(dx_stride=s, dgate_stride=s)
+    assert lrec_backward(lib, p, dx=at(7), dz=at(7, 48), nws=16) == "GDN_ERR_WORKSPACE_TOO_SMALL"
+    assert lrec_backward(lib, p, dx=at(7), dz=at(7, 46)) == "GDN_ERR_ALIASING"
+
+
+def test_lrec_step_refusals(lib):
+    p = lrec_problem()
+
+    def step(p, x=at(0), z=at(1), state=at(2), o=at(3)):
+        return name(lib.gdn_lrec_step(p, x, z, state, o, None))
+
+    assert step(ctypes.byref(p)) == "GDN_ERR_BAD_SHAPE"                    # L != 1
+    one = block.make_lrec_problem(2, 1, 24)
+    assert step(None) == "GDN_ERR_NULL_POINTER"
+    for arg in ("x", "z", "state", "o"):
+        assert step(ctypes.byref(one), **{arg: None}) == "GDN_ERR_NULL_POINTER", arg
+    assert step(ctypes.byref(one), state=at(0)) == "GDN_ERR_ALIASING"
+    assert block.lrec_workspace_size(one, gb.GDN_OP_STEP) == 0
+    n = ctypes.c_size_t(0)
+    assert name(lib.gdn_lrec_workspace_size(ctypes.byref(p), gb.GDN_OP_STEP,
+                                            ctypes.byref(n))) == "GDN_ERR_BAD_SHAPE"
+    assert name(lib.gdn_lrec_workspace_size(ctypes.byref(p), 3,
+                                            ctypes.byref(n))) == "GDN_ERR_BAD_SHAPE"
+
+
+# ---- the binding's own checks ----
+
+def test_qk_plan_checks_every_tensor(lib):
+    B, L, Hq, Hk, D = 2, 3, 4, 2, 32
+    plan = block.QkPlan(B, L, Hq, Hk, D, "bf16", "cpu", axis_pairs=(8,), weights=True,
+                        backward=True)
+    bf = torch.bfloat16
+    good = dict(q=torch.zeros((B, L, Hq, D), dtype=bf), k=torch.zeros((B, L, Hk, D), dtype=bf),
+                positions=torch.zeros((B, L, 1), dtype=torch.int32), q_weight=torch.zeros(D),
+                k_weight=torch.zeros(D), lengths=torch.zeros(B, dtype=torch.int32))
+    grads = dict(d_q=good["q"], d_k=good["k"])
+    wrong = [
+        ({"q": good["q"].float()}, TypeError), ({"q": good["q"][:, :, 1:]}, ValueError),
+        ({"k": good["k"].transpose(2, 3).contiguous().transpose(2, 3)}, ValueError),
+        ({"k": None}, ValueError), ({"positions": None}, ValueError),
+        ({"positions": good["positions"].long()}, TypeError),
+        ({"positions": good["positions"][:, 1:]}, ValueError),
+        ({"q_weight": torch.zeros(D, dtype=bf)}, TypeError),
+        ({"k_weight": torch.zeros(D + 1)}, ValueError),
+        ({"lengths": good["lengths"][1:]}, ValueError),
+        ({"q": block.Checkpoint(good["q"], good["q"])}, TypeError),
+        ({"q": block.Checkpoint(good["q"], good["q"]),
+          "k": block.Checkpoint(good["k"], good["k"])}, TypeError),
+    ]
+    for over, exc in wrong:
+        with pytest.raises(exc):
+            plan.forward(**dict(good, **over))
+        with pytest.raises(exc):
+            plan.backward(**grads, **dict(good, **over))
+    for over, exc in (({"d_q": good["q"].float()}, TypeError), ({"d_k": None}, ValueError),
+                      ({"dq": good["k"]}, ValueError)):
+        with pytest.raises(exc):
+            plan.backward(**dict(grads, **good, **over))
+    with pytest.raises(ValueError):
+        block.QkPlan(B, L, Hq, Hk, D, "bf16", "cpu", axis_pairs=(2, 2, 2, 2))
+    with pytest.raises(gb.GdnError):
+        block.QkPlan(B, L, Hq, Hk, D, "bf16", "cpu", axis_pairs=(17,))
+
+
+def test_lrec_plan_checks_every_tensor(lib):
+    B, L, C = 2, 3, 8
+    plan = block.LrecPlan(B, L, C, "fp32", "cpu", saved=True, backward=True)
+    x, h = torch.zeros((B, L, C)), torch.zeros((B, C))
+    good = dict(x=x, gate=x, state=h, lengths=torch.zeros(B, dtype=torch.int32))
+    wrong = [({"x": x.bfloat16()}, TypeError), ({"gate": x[:, 1:]}, ValueError),
+             ({"x": x.transpose(1, 2).contiguous().transpose(1, 2)}, ValueError),
+             ({"state": h.double()}, TypeError), ({"state": h.t().contiguous().t()}, ValueError),
+             ({"lengths": torch.zeros(B)}, TypeError), ({"gate": None}, ValueError)]
+    for over, exc in wrong:
+        with pytest.raises(exc):
+            plan.forward(**dict(good, **over))
+        with pytest.raises(exc):
+            plan.backward(d_o=x, **dict(good, **over))
+    for over, exc in (({"d_o": x[:, 1:]}, ValueError), ({"d_state": h[:, 1:]}, ValueError),
+                      ({"saved": plan.saved[1:]}, ValueError), ({"dx": x.double()}, TypeError)):
+        with pytest.raises(exc):
+            plan.backward(**dict(dict(good, d_o=x), **over))
+    with pytest.raises(ValueError):
+        block.LrecPlan(B, L, C, "fp32", "cpu").backward(x, x, x)
+    with pytest.raises(ValueError):
+        block.LrecPlan(B, 1, C, "fp32", "cpu").step(x[:, :1], x[:, :1], None)
+
+
+def test_checkpoint_checks(lib):
+    x = torch.zeros((1, 2, 3, 16), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        block.pack8(x[0])
+    with pytest.raises(TypeError):
+        block.pack8(x.half())
+    v, s = torch.zeros((1, 2, 3, 16), dtype=torch.uint8), torch.zeros((1, 2, 3), dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        block.unpack8(block.Checkpoint(v, s))
+    with pytest.raises(ValueError):
+        block.unpack8(block.Checkpoint(v.view(torch.float8_e4m3fn), s[:, 1:]))
+    with pytest.raises(TypeError):
+        block.unpack8(block.Checkpoint(v.view(torch.float8_e4m3fn), s), torch.float16)

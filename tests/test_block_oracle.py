@@ -1,0 +1,147 @@
+"""CPU pins of the block's float64 oracle: closed forms, brute force, the
+e4m3 format's own numbers, and central differences of every gradient."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_oracle as bo
+
+
+def _rng(seed):
+    return np.random.Generator(np.random.PCG64(seed))
+
+
+def test_rotation_is_a_complex_product():
+    rng = _rng(0)
+    pos = rng.integers(-50, 50, (2, 3, 2))
+    phi = bo.qk_angles(pos, (2, 4), 100.0)
+    assert phi.shape == (2, 3, 6)
+    assert phi[1, 2, 0] == pos[1, 2, 0] and phi[1, 2, 2] == pos[1, 2, 1]
+    assert np.isclose(phi[1, 2, 1], pos[1, 2, 0] * 100.0 ** -0.5)
+    x = rng.standard_normal((2, 3, 4, 16))
+    for pairing in ("halves", "adjacent"):
+        y, _ = bo.qk_forward(x, None, phi, "none", 0.0, pairing)
+        v = x[..., :6] + 1j * x[..., 6:12] if pairing == "halves" else \
+            x[..., 0:12:2] + 1j * x[..., 1:12:2]
+        v = v * np.exp(1j * phi)[:, :, None]
+        got = y[..., :6] + 1j * y[..., 6:12] if pairing == "halves" else \
+            y[..., 0:12:2] + 1j * y[..., 1:12:2]
+        assert np.allclose(got, v) and np.array_equal(y[..., 12:], x[..., 12:])
+        # a turn by any angle keeps the rows' norms
+        z, _ = bo.qk_forward(x, None, phi + 7.0, "none", 0.0, pairing)
+        assert np.allclose(np.sum(y * y, -1), np.sum(z * z, -1))
+
+
+@pytest.mark.parametrize("norm,eps", [("l2", 0.0), ("rms", 1e-6)])
+def test_norms(norm, eps):
+    x = _rng(1).standard_normal((1, 2, 3, 8))
+    x[0, 0, 0] = 0.0
+    y, _ = bo.qk_forward(x, np.full(8, 2.0), None, norm, eps, "halves")
+    assert np.array_equal(y[0, 0, 0], np.zeros(8))
+    want = 2.0 if norm == "l2" else 2.0 * np.sqrt(8)
+    assert np.allclose(np.linalg.norm(y[0, 1], axis=-1), want, rtol=1e-5)
+
+
+def _differences(f, x, g, n=25, eps=1e-6, seed=5):
+    """Central differences of sum(f(x)) against the gradient g at n places."""
+    rng = _rng(seed)
+    for _ in range(n):
+        i = tuple(rng.integers(0, s) for s in x.shape)
+        p, m = x.copy(), x.copy()
+        p[i] += eps
+        m[i] -= eps
+        d = (f(p) - f(m)) / (2 * eps)
+        assert abs(d - g[i]) <= 1e-6 * max(1.0, abs(d)), (i, d, g[i])
+
+
+@pytest.mark.parametrize("norm", ["none", "l2", "rms"])
+@pytest.mark.parametrize("pairing", ["halves", "adjacent"])
+def test_qk_gradient_by_differences(norm, pairing):
+    rng = _rng(2)
+    x, dy = rng.standard_normal((2, 3, 2, 12)), rng.standard_normal((2, 3, 2, 12))
+    w = None if norm == "none" else 1.0 + 0.3 * rng.standard_normal(12)
+    phi = rng.standard_normal((2, 3, 4))
+    (dx, dw), _ = bo.qk_backward(x, w, phi, norm, 1e-3, pairing, dy)
+    _differences(lambda v: np.sum(dy * bo.qk_forward(v, w, phi, norm, 1e-3, pairing)[0]), x, dx)
+    if w is not None:
+        _differences(lambda v: np.sum(dy * bo.qk_forward(x, v, phi, norm, 1e-3, pairing)[0]), w,
+                     dw)
+
+
+def test_e4m3_is_the_formats():
+    v = bo.e4m3_values()
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(np.isnan(v), np.isnan(t))
+    assert np.array_equal(v[~np.isnan(v)], t[~np.isnan(t)])
+
+
+def test_pack8_rounds_to_nearest_and_scales_by_powers_of_two():
+    rng = _rng(3)
+    x = (rng.standard_normal((40, 32)) * np.exp(3 * rng.standard_normal((40, 1)))).astype(np.float32)
+    x[0] = 0.0
+    x[1] *= 1e-30
+    x[2, 3], x[2, 4] = np.inf, np.nan
+    v, s = bo.pack8(x)
+    assert s[0] == 0 and not v[0].any() and v[2, 3] == 127 and v[2, 4] == 127
+    back = bo.unpack8(v, s)
+    fin = np.isfinite(x)
+    amax = np.max(np.where(fin, np.abs(x), 0), axis=-1)
+    for i in range(1, 40):
+        top = 448.0 * 2.0 ** (int(s[i]) - 127)
+        assert amax[i] <= top and (amax[i] > top / 2 or s[i] == 0)
+        # half a step: 2^-4 relative, or half the subnormal step 2^-9 2^e
+        step = np.maximum(np.abs(x[i]) * 2.0 ** -4, 2.0 ** -10 * 2.0 ** (int(s[i]) - 127))
+        assert np.all(np.abs(back[i] - x[i])[fin[i]] <= step[fin[i]])
+    # torch's conversion of the scaled values agrees byte for byte
+    scaled = torch.from_numpy(np.ldexp(x, (127 - s.astype(np.int32))[:, None]))
+    ok = torch.from_numpy(fin)
+    b = scaled.to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(b[ok], torch.from_numpy(v)[ok])
+
+
+def test_lrec_closed_forms():
+    x = _rng(4).standard_normal((2, 9, 3))
+    ones = np.ones_like(x)
+    (o, h), _ = bo.lrec_forward(x, ones, False, False)
+    assert np.allclose(o, np.cumsum(x, axis=1)) and np.allclose(h, x.sum(1))
+    (o, _), _ = bo.lrec_forward(x, 0.0 * ones, False, False, h0=np.ones((2, 3)))
+    assert np.array_equal(o, x)
+    # a constant input with the complement converges to itself from any state
+    (o, _), _ = bo.lrec_forward(ones, 0.3 * ones, False, True, h0=np.full((2, 3), 5.0))
+    assert np.allclose(o, 1.0 + 4.0 * 0.3 ** np.arange(1, 10)[None, :, None])
+    # brute force
+    z = _rng(5).standard_normal((2, 9, 3))
+    a = 1 / (1 + np.exp(-z))
+    (o, _), _ = bo.lrec_forward(x, z, True, True)
+    want = sum(np.prod(a[:, s + 1:7], axis=1) * (1 - a[:, s]) * x[:, s] for s in range(7))
+    assert np.allclose(o[:, 6], want)
+
+
+def test_lrec_lengths():
+    rng = _rng(6)
+    x, z, h0 = rng.standard_normal((4, 6, 2)), rng.standard_normal((4, 6, 2)), \
+        rng.standard_normal((4, 2))
+    (o, h), _ = bo.lrec_forward(x, z, True, True, h0, [6, 0, 1, 99])
+    (o3, h3), _ = bo.lrec_forward(x[2:3, :1], z[2:3, :1], True, True, h0[2:3])
+    assert np.array_equal(h[1], h0[1]) and not o[1].any()
+    assert np.array_equal(o[2, :1], o3[0]) and np.array_equal(h[2], h3[0]) and not o[2, 1:].any()
+
+
+@pytest.mark.parametrize("logits", [False, True])
+@pytest.mark.parametrize("complement", [False, True])
+def test_lrec_gradient_by_differences(logits, complement):
+    rng = _rng(7)
+    B, L, C = 3, 7, 2
+    x, z, d = (rng.standard_normal((B, L, C)) for _ in range(3))
+    h0, dh = rng.standard_normal((B, C)), rng.standard_normal((B, C))
+    n = [7, 4, 1]
+
+    def loss(x, z, h0):
+        (o, h), _ = bo.lrec_forward(x, z, logits, complement, h0, n)
+        return np.sum(o * d) + np.sum(h * dh)
+
+    (dx, dz, dh0), _ = bo.lrec_backward(x, z, logits, complement, d, h0, dh, n)
+    _differences(lambda v: loss(v, z, h0), x, dx)
+    _differences(lambda v: loss(x, v, h0), z, dz)
+    _differences(lambda v: loss(x, z, v), h0, dh0)
