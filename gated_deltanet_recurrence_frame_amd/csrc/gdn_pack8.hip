@@ -11,6 +11,15 @@ constexpr int kPackThreads = 256;
 constexpr int kPackWaves = kPackThreads / 64;
 constexpr int kPackRows = 4;    // rows of a lane in flight
 
+// Row r (of B L H) of the strided tensor.
+template <int IO>
+__device__ __forceinline__ const char* io_row(const PackArgs& a, uint32_t r) {
+  const uint32_t tok = r / (uint32_t)a.H, h = r - tok * (uint32_t)a.H;
+  const uint32_t b = tok / (uint32_t)a.L, l = tok - b * (uint32_t)a.L;
+  return static_cast<const char*>(a.x.p) +
+         ((int64_t)b * a.x.sb + (int64_t)l * a.x.sl + (int64_t)h * a.row.D) * Io<IO>::bytes;
+}
+
 template <int IO, int V>
 __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
   const int rpw = 64 / a.row.group;
@@ -18,34 +27,28 @@ __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const bool in_row = j < a.row.lanes;
   const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
-  float f[kPackRows][2 * V];
+  const Slot at = {2 * j * V, 2 * j * V + V};
+  IoRow<IO, V> x[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
-#pragma unroll
-    for (int e = 0; e < 2 * V; ++e) f[i][e] = 0.f;
-    if (in_row && r < rows) {
-      const uint32_t tok = r / (uint32_t)a.H, h = r - tok * (uint32_t)a.H;
-      const uint32_t b = tok / (uint32_t)a.L, l = tok - b * (uint32_t)a.L;
-      const char* p = static_cast<const char*>(a.x.p) +
-                      ((int64_t)b * a.x.sb + (int64_t)l * a.x.sl + (int64_t)h * a.row.D +
-                       2 * j * V) * Io<IO>::bytes;
-      row_load<IO, V>(p, f[i]);
-      row_load<IO, V>(p + V * Io<IO>::bytes, f[i] + V);
-    }
+    x[i].clear();
+    if (in_row && r < rows) x[i].load(io_row<IO>(a, r), at);
   }
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
-    const int s = scale_byte(group_max(finite_max<2 * V>(f[i]), a.row.group));
+    const int s = scale_byte(group_max(row_max<IO, V>(x[i]), a.row.group));
     const float m = pack_factor(s);
+    float f[2 * V];
+    x[i].get(f);
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) f[i][e] *= m;
+    for (int e = 0; e < 2 * V; ++e) f[e] *= m;
     if (r < rows) {
       if (in_row) {
-        uint8_t* v = static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D + 2 * j * V;
-        e4m3_store<V>(v, f[i]);
-        e4m3_store<V>(v + V, f[i] + V);
+        uint8_t* v = static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D;
+        e4m3_store<V>(v + at.a, f);
+        e4m3_store<V>(v + at.b, f + V);
       }
       if (j == 0) static_cast<uint8_t*>(a.scale)[r] = (uint8_t)s;
     }
@@ -59,15 +62,14 @@ __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
   if (j >= a.row.lanes) return;
-  float f[kPackRows][2 * V];
+  const Slot at = {2 * j * V, 2 * j * V + V};
+  E4m3Row<V> v[kPackRows];
   float m[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
     if (r < rows) {
-      const uint8_t* v = static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D + 2 * j * V;
-      e4m3_load<V>(v, f[i]);
-      e4m3_load<V>(v + V, f[i] + V);
+      v[i].load(static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D, at);
       m[i] = unpack_factor(static_cast<const uint8_t*>(a.scale)[r]);
     }
   }
@@ -75,15 +77,13 @@ __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
     if (r < rows) {
+      float f[2 * V];
+      v[i].get(f);
 #pragma unroll
-      for (int e = 0; e < 2 * V; ++e) f[i][e] *= m[i];
-      const uint32_t tok = r / (uint32_t)a.H, h = r - tok * (uint32_t)a.H;
-      const uint32_t b = tok / (uint32_t)a.L, l = tok - b * (uint32_t)a.L;
-      char* p = const_cast<char*>(static_cast<const char*>(a.x.p)) +
-                ((int64_t)b * a.x.sb + (int64_t)l * a.x.sl + (int64_t)h * a.row.D + 2 * j * V) *
-                    Io<IO>::bytes;
-      row_store<IO, V>(p, f[i]);
-      row_store<IO, V>(p + V * Io<IO>::bytes, f[i] + V);
+      for (int e = 0; e < 2 * V; ++e) f[e] *= m[i];
+      char* p = const_cast<char*>(io_row<IO>(a, r));
+      row_store<IO, V>(p + at.a * Io<IO>::bytes, f);
+      row_store<IO, V>(p + at.b * Io<IO>::bytes, f + V);
     }
   }
 }

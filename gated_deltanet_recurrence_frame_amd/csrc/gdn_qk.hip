@@ -1,8 +1,8 @@
 // Queries and keys of a projection: norm per head and rotation by position
 // in one pass (gdn_qk_forward), and its gradient (gdn_qk_backward).
 //
-// A wave takes one token at a time: its H_q + H_k rows lie next to each other
-// over groups of lanes (RowShape), 64 / group rows a step.  The rotation's
+// A wave takes one token after the other: the rows of its heads lie next to
+// each other over groups of lanes (RowShape), 64 / group rows a step.  The rotation's
 // cosines and sines are the same for every head of a token, so the wave's
 // lanes form one pair's each, once a token (the angle in turns in 64 bits,
 // reduced to (-1/2, 1/2] before it is rounded), and pass them through LDS;
@@ -14,47 +14,52 @@ namespace gdn {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkWaves = kQkThreads / 64;
-constexpr int kQkRows = 4;          // rows of a lane in flight (forward)
-constexpr int kQkBackRows = 2;      // (backward)
-constexpr int kQkBackWgs = 1024;    // workgroups of the backward pass at most
+constexpr int kQkAhead = 4;         // steps loaded ahead (forward)
+constexpr int kQkBackAhead = 3;     // (backward)
+constexpr int kQkWgs = 1024;        // workgroups of the forward pass at most
+constexpr int kQkBackWgs = 512;     // of the backward pass, for each operand
 constexpr int kMaxPairs = kRowMaxD / 2;
 
-// One operand's member of a pair of arguments, by a select: the operand
-// differs between lanes, and an indexed argument would be a load a lane.
-template <typename T>
-__device__ __forceinline__ T pick(const T (&p)[2], bool second) {
-  return second ? p[1] : p[0];
-}
-__device__ __forceinline__ RowView pick(const RowView (&p)[2], bool second) {
-  return RowView{second ? p[1].p : p[0].p, second ? p[1].sb : p[0].sb,
-                 second ? p[1].sl : p[0].sl};
-}
-
-struct TokenAt {
+// Where a wave stands: a token, and a step of its rows (64 / group heads of
+// one operand).  The same for all lanes.
+struct Cursor {
   uint32_t tok, b, l;
-  bool live;
+  int step;
+  bool live;       // before the sequence's end
 };
-__device__ __forceinline__ TokenAt token_at(const QkArgs& a, uint32_t tok) {
-  TokenAt t;
-  t.tok = tok;
-  t.b = a.B == 1 ? 0u : tok / (uint32_t)a.L;
-  t.l = tok - t.b * (uint32_t)a.L;
-  t.live = !a.len || (int)t.l < a.len[t.b];
-  return t;
+__device__ __forceinline__ void set_token(const QkArgs& a, Cursor* c, uint32_t tok) {
+  c->tok = tok;
+  c->step = 0;
+  c->b = a.B == 1 ? 0u : tok / (uint32_t)a.L;
+  c->l = tok - c->b * (uint32_t)a.L;
+  c->live = !a.len || tok >= (uint32_t)a.B * a.L || (int)c->l < a.len[c->b];
+}
+__device__ __forceinline__ void advance(const QkArgs& a, Cursor* c, int steps, uint32_t waves) {
+  if (++c->step == steps) set_token(a, c, c->tok + waves);
 }
 
-// The token's cosines and sines into LDS: trig[2 m], trig[2 m + 1] of pair m.
-__device__ __forceinline__ void token_turns(const QkArgs& a, const TokenAt& t, float* trig) {
-  const int32_t* pos = a.pos + (int64_t)(a.pos_shared ? t.l : t.tok) * a.axes;
-  for (int m = lane_id(); m < a.pairs; m += 64) {
-    const int axis = m < a.bound1 ? 0 : m < a.bound2 ? 1 : 2;
-    double turn = (double)pos[axis] * a.turns[m];
-    turn -= rint(turn);
-    float s, c;
-    sincospif(2.f * (float)turn, &s, &c);
-    trig[2 * m] = c;
-    trig[2 * m + 1] = s;
+// A lane's share of the rotation: one pair (two in heads beyond 128).
+struct Turns {
+  double per[2];   // turns per unit of position
+  int axis[2];
+  int pos[2];      // of the token to come
+};
+__device__ __forceinline__ void turns_init(const QkArgs& a, Turns* t) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = lane_id() + 64 * i;
+    t->per[i] = m < a.pairs ? a.turns[m] : 0.0;
+    t->axis[i] = m < a.bound1 ? 0 : m < a.bound2 ? 1 : 2;
+    t->pos[i] = 0;
   }
+}
+__device__ __forceinline__ void turns_fetch(const QkArgs& a, Turns* t, uint32_t tok) {
+  if (tok >= (uint32_t)a.B * a.L) return;
+  const uint32_t row = a.pos_shared ? tok % (uint32_t)a.L : tok;
+  const int32_t* pos = a.pos + (int64_t)row * a.axes;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane_id() + 64 * i < a.pairs) t->pos[i] = pos[t->axis[i]];
 }
 
 // LDS written by a wave's lanes and read by others of the same wave.
@@ -62,6 +67,33 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The token's cosines and sines, through LDS to the lanes' V pairs each:
+// trig[2 m], trig[2 m + 1] of pair m.
+template <int V>
+__device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, float* trig, int j,
+                                            float* c, float* s) {
+  wave_lds_sync();   // the last token's reads are done
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = lane_id() + 64 * i;
+    if (m < a.pairs) {
+      double turn = (double)t.pos[i] * t.per[i];
+      turn -= rint(turn);
+      float sn, cs;
+      sincospif(2.f * (float)turn, &sn, &cs);
+      trig[2 * m] = cs;
+      trig[2 * m + 1] = sn;
+    }
+  }
+  wave_lds_sync();
+  const bool turned = j * V < a.pairs;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    c[e] = turned ? trig[2 * (j * V + e)] : 1.f;
+    s[e] = turned ? trig[2 * (j * V + e) + 1] : 0.f;
+  }
 }
 
 // Turn a lane's V pairs by phi (SIGN 1) or -phi (SIGN -1).
@@ -84,15 +116,25 @@ __device__ __forceinline__ void turn(float* f, const float* c, const float* s, b
   }
 }
 
+// 1 / sqrt of a row's argument; 0 where that is 0, NaN stays.
+__device__ __forceinline__ float row_inverse(float ss) {
+  return ss > 0.f ? 1.f / sqrtf(ss) : ss;
+}
+
 // The operands' weights side by side: [2][kRowMaxD], 1 where there are none.
 __device__ __forceinline__ void stage_weights(const QkArgs& a, float* w) {
   for (int i = threadIdx.x; i < 2 * a.row.D; i += kQkThreads) {
     const int which = i >= a.row.D, d = i - which * a.row.D;
-    w[which * kRowMaxD + d] = a.w[which] ? a.w[which][d] : 1.f;
+    const float* p = which ? a.w[1] : a.w[0];
+    w[which * kRowMaxD + d] = p ? p[d] : 1.f;
   }
   __syncthreads();
 }
 
+template <int IO, int V, bool PACKED> struct Source { typedef IoRow<IO, V> row; };
+template <int IO, int V> struct Source<IO, V, true> { typedef E4m3Row<V> row; };
+
+// Rows are loaded kQkAhead steps before they are used.
 template <int IO, int V, bool PACKED>
 __global__ __launch_bounds__(kQkThreads) void qk_forward_kernel(QkArgs a) {
   __shared__ float trig_all[kQkWaves][2 * kMaxPairs];
@@ -100,251 +142,243 @@ __global__ __launch_bounds__(kQkThreads) void qk_forward_kernel(QkArgs a) {
   constexpr int ES = Io<IO>::bytes;
   const bool weighted = a.w[0] || a.w[1];
   if (weighted) stage_weights(a, w);
-  const int wv = wave_id(), lane = lane_id(), j = lane & (a.row.group - 1);
+  const int lane = lane_id(), j = lane & (a.row.group - 1);
   const int rg = lane / a.row.group, rpw = 64 / a.row.group;
-  const bool in_row = j < a.row.lanes, turned = j * V < a.pairs;
+  const bool in_row = j < a.row.lanes;
   const Slot at = row_slot<V>(j, a.pairs, a.adjacent);
-  const uint32_t tokens = (uint32_t)a.B * a.L;
-  const int rows = a.H[0] + a.H[1];
-  float* trig = trig_all[wv];
+  const uint32_t tokens = (uint32_t)a.B * a.L, waves = gridDim.x * kQkWaves;
+  const int nq = (a.H[0] + rpw - 1) / rpw, steps = nq + (a.H[1] + rpw - 1) / rpw;
+  float* trig = trig_all[wave_id()];
 
-  for (uint32_t tok = blockIdx.x * kQkWaves + wv; tok < tokens; tok += gridDim.x * kQkWaves) {
-    const TokenAt t = token_at(a, tok);
-    float c[V], s[V];
-    if (a.pairs) {
-      wave_lds_sync();   // the last token's reads are done
-      if (t.live) token_turns(a, t, trig);
-      wave_lds_sync();
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        c[e] = turned ? trig[2 * (j * V + e)] : 1.f;
-        s[e] = turned ? trig[2 * (j * V + e) + 1] : 0.f;
+  typename Source<IO, V, PACKED>::row ahead[kQkAhead];
+  int scale[kQkAhead];
+  Cursor ld, at_step;
+  Turns turns;
+  set_token(a, &ld, blockIdx.x * kQkWaves + wave_id());
+  at_step = ld;
+  if (a.pairs) {
+    turns_init(a, &turns);
+    turns_fetch(a, &turns, ld.tok);
+  }
+  auto load = [&](int i) {
+    const bool second = ld.step >= nq;
+    const int h = (ld.step - (second ? nq : 0)) * rpw + rg, heads = second ? a.H[1] : a.H[0];
+    ahead[i].clear();
+    scale[i] = 0;
+    if (in_row && h < heads && ld.tok < tokens && ld.live) {
+      if constexpr (PACKED) {
+        const int64_t row = (int64_t)ld.tok * heads + h;
+        ahead[i].load((second ? a.v8[1] : a.v8[0]) + row * a.row.D, at);
+        scale[i] = (second ? a.s8[1] : a.s8[0])[row];
+      } else {
+        const RowView& x = second ? a.x[1] : a.x[0];
+        ahead[i].load(static_cast<const char*>(x.p) +
+                          ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl) * ES +
+                          h * a.row.D * ES,
+                      at);
       }
     }
-    for (int r0 = 0; r0 < rows; r0 += rpw * kQkRows) {
-      float f[kQkRows][2 * V];
-      float m[kQkRows];
+    advance(a, &ld, steps, waves);
+  };
 #pragma unroll
-      for (int i = 0; i < kQkRows; ++i) {
-        const int r = r0 + i * rpw + rg;
-        const bool which = r >= a.H[0];
-        const int h = r - (which ? a.H[0] : 0);
+  for (int i = 0; i < kQkAhead; ++i) load(i);
+
+  float c[V], s[V];
+  while (at_step.tok < tokens) {
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) f[i][e] = 0.f;
-        m[i] = 0.f;
-        if (in_row && r < rows && t.live) {
-          if constexpr (PACKED) {
-            const int64_t row = (int64_t)tok * (which ? a.H[1] : a.H[0]) + h;
-            const uint8_t* p = pick(a.v8, which) + row * a.row.D;
-            e4m3_load<V>(p + at.a, f[i]);
-            e4m3_load<V>(p + at.b, f[i] + V);
-            m[i] = unpack_factor(pick(a.s8, which)[row]);
-          } else {
-            const RowView x = pick(a.x, which);
-            const char* p = static_cast<const char*>(x.p) +
-                            ((int64_t)t.b * x.sb + (int64_t)t.l * x.sl + h * a.row.D) * ES;
-            row_load<IO, V>(p + at.a * ES, f[i]);
-            row_load<IO, V>(p + at.b * ES, f[i] + V);
-          }
-        }
+    for (int i = 0; i < kQkAhead; ++i) {
+      if (at_step.tok >= tokens) break;
+      if (at_step.step == 0 && a.pairs) {
+        token_turns<V>(a, turns, trig, j, c, s);
+        turns_fetch(a, &turns, at_step.tok + waves);
       }
+      const bool second = at_step.step >= nq;
+      const int h = (at_step.step - (second ? nq : 0)) * rpw + rg;
+      const int heads = second ? a.H[1] : a.H[0];
+      const bool put = in_row && h < heads;
+      const int64_t row = (int64_t)at_step.tok * heads + h;
+      float f[2 * V];
+      ahead[i].get(f);
+      if constexpr (PACKED) {
+        const float m = unpack_factor(scale[i]);
 #pragma unroll
-      for (int i = 0; i < kQkRows; ++i) {
-        const int r = r0 + i * rpw + rg;
-        if (r0 + i * rpw >= rows) break;
-        const bool which = r >= a.H[0];
-        const int h = r - (which ? a.H[0] : 0);
-        const bool put = in_row && r < rows;
-        const int64_t row = (int64_t)tok * (which ? a.H[1] : a.H[0]) + h;
-        if constexpr (PACKED) {
+        for (int e = 0; e < 2 * V; ++e) f[e] *= m;
+      } else if (a.v8_out[0]) {
+        const int sb = scale_byte(group_max(row_max<IO, V>(ahead[i]), a.row.group));
+        const float k = pack_factor(sb);
+        float g[2 * V];
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e) f[i][e] *= m[i];
-        }
-        if (!PACKED && a.v8_out[0]) {
-          const int sb = scale_byte(group_max(finite_max<2 * V>(f[i]), a.row.group));
-          const float k = pack_factor(sb);
-          float g[2 * V];
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) g[e] = f[i][e] * k;
-          if (put) {
-            e4m3_store<V>(pick(a.v8_out, which) + row * a.row.D + at.a, g);
-            e4m3_store<V>(pick(a.v8_out, which) + row * a.row.D + at.b, g + V);
-            if (j == 0) pick(a.s8_out, which)[row] = (uint8_t)sb;
-          }
-        }
-        if (a.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[i][e], f[i][e], ss);
-          ss = fmaf(group_sum(ss, a.row.group), a.c, a.eps);
-          const float inv = ss > 0.f ? 1.f / sqrtf(ss) : ss == 0.f ? 0.f : ss;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) f[i][e] *= inv;
-          if (weighted && in_row) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              f[i][e] *= w[which * kRowMaxD + at.a + e];
-              f[i][e + V] *= w[which * kRowMaxD + at.b + e];
-            }
-          }
-        }
-        if (a.pairs) turn<V, 1>(f[i], c, s, a.adjacent);
+        for (int e = 0; e < 2 * V; ++e) g[e] = f[e] * k;
         if (put) {
-          if (!t.live) {
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) f[i][e] = 0.f;
-          }
-          char* p = static_cast<char*>(pick(a.y, which)) + row * a.row.D * ES;
-          row_store<IO, V>(p + at.a * ES, f[i]);
-          row_store<IO, V>(p + at.b * ES, f[i] + V);
+          uint8_t* v = (second ? a.v8_out[1] : a.v8_out[0]) + row * a.row.D;
+          e4m3_store<V>(v + at.a, g);
+          e4m3_store<V>(v + at.b, g + V);
+          if (j == 0) (second ? a.s8_out[1] : a.s8_out[0])[row] = (uint8_t)sb;
         }
       }
+      if (a.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
+        const float inv = row_inverse(fmaf(group_sum(ss, a.row.group), a.c, a.eps));
+#pragma unroll
+        for (int e = 0; e < 2 * V; ++e) f[e] *= inv;
+        if (weighted && in_row) {
+          const float* wv = w + (second ? kRowMaxD : 0);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            f[e] *= wv[at.a + e];
+            f[e + V] *= wv[at.b + e];
+          }
+        }
+      }
+      if (a.pairs) turn<V, 1>(f, c, s, a.adjacent);
+      if (put) {
+        if (!at_step.live) {
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) f[e] = 0.f;
+        }
+        char* p = static_cast<char*>(second ? a.y[1] : a.y[0]) + row * a.row.D * ES;
+        row_store<IO, V>(p + at.a * ES, f);
+        row_store<IO, V>(p + at.b * ES, f + V);
+      }
+      load(i);
+      advance(a, &at_step, steps, waves);
     }
   }
 }
 
+// One operand a workgroup (blockIdx.y), so that its weights and the sums of
+// their gradients are one set of registers.
 template <int IO, int V, bool PACKED>
 __global__ __launch_bounds__(kQkThreads) void qk_backward_kernel(QkArgs a) {
   __shared__ float trig_all[kQkWaves][2 * kMaxPairs];
-  __shared__ float w[2 * kRowMaxD];
+  __shared__ float sum[kRowMaxD];
   constexpr int ES = Io<IO>::bytes;
-  const bool weighted = a.w[0] || a.w[1];
-  if (weighted) stage_weights(a, w);
-  const int wv = wave_id(), lane = lane_id(), j = lane & (a.row.group - 1);
+  const bool second = blockIdx.y;
+  const int heads = second ? a.H[1] : a.H[0];
+  const RowView x = second ? a.x[1] : a.x[0], dx = second ? a.dx[1] : a.dx[0];
+  const uint8_t* v8 = second ? a.v8[1] : a.v8[0];
+  const uint8_t* s8 = second ? a.s8[1] : a.s8[0];
+  const char* dy = static_cast<const char*>(second ? a.y[1] : a.y[0]);
+  const float* wp = second ? a.w[1] : a.w[0];
+  const int lane = lane_id(), j = lane & (a.row.group - 1);
   const int rg = lane / a.row.group, rpw = 64 / a.row.group;
-  const bool in_row = j < a.row.lanes, turned = j * V < a.pairs;
+  const bool in_row = j < a.row.lanes;
   const Slot at = row_slot<V>(j, a.pairs, a.adjacent);
-  const uint32_t tokens = (uint32_t)a.B * a.L;
-  const int rows = a.H[0] + a.H[1];
-  float* trig = trig_all[wv];
-  float dwq[2 * V], dwk[2 * V];   // this lane's columns of the weights' gradients
+  const uint32_t tokens = (uint32_t)a.B * a.L, waves = gridDim.x * kQkWaves;
+  const int steps = (heads + rpw - 1) / rpw;
+  float* trig = trig_all[wave_id()];
+  float w[2 * V], dw[2 * V];
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) dwq[e] = dwk[e] = 0.f;
+  for (int e = 0; e < 2 * V; ++e) {
+    w[e] = wp && in_row ? wp[e < V ? at.a + e : at.b + e - V] : 1.f;
+    dw[e] = 0.f;
+  }
 
-  for (uint32_t tok = blockIdx.x * kQkWaves + wv; tok < tokens; tok += gridDim.x * kQkWaves) {
-    const TokenAt t = token_at(a, tok);
-    float c[V], s[V];
-    if (a.pairs) {
-      wave_lds_sync();
-      if (t.live) token_turns(a, t, trig);
-      wave_lds_sync();
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        c[e] = turned ? trig[2 * (j * V + e)] : 1.f;
-        s[e] = turned ? trig[2 * (j * V + e) + 1] : 0.f;
+  typename Source<IO, V, PACKED>::row xs[kQkBackAhead];
+  IoRow<IO, V> gs[kQkBackAhead];
+  int scale[kQkBackAhead];
+  Cursor ld, at_step;
+  Turns turns;
+  set_token(a, &ld, blockIdx.x * kQkWaves + wave_id());
+  at_step = ld;
+  if (a.pairs) {
+    turns_init(a, &turns);
+    turns_fetch(a, &turns, ld.tok);
+  }
+  auto load = [&](int i) {
+    const int h = ld.step * rpw + rg;
+    xs[i].clear();
+    gs[i].clear();
+    scale[i] = 0;
+    if (in_row && h < heads && ld.tok < tokens && ld.live) {
+      const int64_t row = (int64_t)ld.tok * heads + h;
+      gs[i].load(dy + row * a.row.D * ES, at);
+      if (a.norm) {
+        if constexpr (PACKED) {
+          xs[i].load(v8 + row * a.row.D, at);
+          scale[i] = s8[row];
+        } else {
+          xs[i].load(static_cast<const char*>(x.p) +
+                         ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl) * ES + h * a.row.D * ES,
+                     at);
+        }
       }
     }
-    for (int r0 = 0; r0 < rows; r0 += rpw * kQkBackRows) {
-      float f[kQkBackRows][2 * V], g[kQkBackRows][2 * V];
-      float m[kQkBackRows];
+    advance(a, &ld, steps, waves);
+  };
 #pragma unroll
-      for (int i = 0; i < kQkBackRows; ++i) {
-        const int r = r0 + i * rpw + rg;
-        const bool which = r >= a.H[0];
-        const int h = r - (which ? a.H[0] : 0);
+  for (int i = 0; i < kQkBackAhead; ++i) load(i);
+
+  float c[V], s[V];
+  while (at_step.tok < tokens) {
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) f[i][e] = g[i][e] = 0.f;
-        m[i] = 0.f;
-        if (in_row && r < rows && t.live) {
-          const int64_t row = (int64_t)tok * (which ? a.H[1] : a.H[0]) + h;
-          const char* y = static_cast<const char*>(pick(a.y, which)) + row * a.row.D * ES;
-          row_load<IO, V>(y + at.a * ES, g[i]);
-          row_load<IO, V>(y + at.b * ES, g[i] + V);
-          if (a.norm) {
-            if constexpr (PACKED) {
-              const uint8_t* p = pick(a.v8, which) + row * a.row.D;
-              e4m3_load<V>(p + at.a, f[i]);
-              e4m3_load<V>(p + at.b, f[i] + V);
-              m[i] = unpack_factor(pick(a.s8, which)[row]);
-            } else {
-              const RowView x = pick(a.x, which);
-              const char* p = static_cast<const char*>(x.p) +
-                              ((int64_t)t.b * x.sb + (int64_t)t.l * x.sl + h * a.row.D) * ES;
-              row_load<IO, V>(p + at.a * ES, f[i]);
-              row_load<IO, V>(p + at.b * ES, f[i] + V);
-            }
-          }
-        }
+    for (int i = 0; i < kQkBackAhead; ++i) {
+      if (at_step.tok >= tokens) break;
+      if (at_step.step == 0 && a.pairs) {
+        token_turns<V>(a, turns, trig, j, c, s);
+        turns_fetch(a, &turns, at_step.tok + waves);
       }
+      const int h = at_step.step * rpw + rg;
+      float g[2 * V];
+      gs[i].get(g);
+      if (a.pairs) turn<V, -1>(g, c, s, a.adjacent);
+      if (a.norm) {
+        float f[2 * V], ss = 0.f, dot = 0.f;
+        xs[i].get(f);
+        if constexpr (PACKED) {
+          const float m = unpack_factor(scale[i]);
 #pragma unroll
-      for (int i = 0; i < kQkBackRows; ++i) {
-        const int r = r0 + i * rpw + rg;
-        if (r0 + i * rpw >= rows) break;
-        const bool which = r >= a.H[0];
-        const int h = r - (which ? a.H[0] : 0);
-        if (a.pairs) turn<V, -1>(g[i], c, s, a.adjacent);
-        if (a.norm) {
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            if constexpr (PACKED) f[i][e] *= m[i];
-            ss = fmaf(f[i][e], f[i][e], ss);
-          }
-          ss = fmaf(group_sum(ss, a.row.group), a.c, a.eps);
-          const float inv = ss > 0.f ? 1.f / sqrtf(ss) : ss == 0.f ? 0.f : ss;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) f[i][e] *= inv;     // x r
-          if (a.part) {
-#pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-              const float v = g[i][e] * f[i][e];
-              dwq[e] += which ? 0.f : v;
-              dwk[e] += which ? v : 0.f;
-            }
-          }
-          if (weighted && in_row) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              g[i][e] *= w[which * kRowMaxD + at.a + e];
-              g[i][e + V] *= w[which * kRowMaxD + at.b + e];
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) dot = fmaf(f[i][e], g[i][e], dot);
-          dot = group_sum(dot, a.row.group) * a.c;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) g[i][e] = (g[i][e] - f[i][e] * dot) * inv;
+          for (int e = 0; e < 2 * V; ++e) f[e] *= m;
         }
-        if (in_row && r < rows) {
-          if (!t.live) {
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) g[i][e] = 0.f;
-          }
-          const RowView d = pick(a.dx, which);
-          char* p = const_cast<char*>(static_cast<const char*>(d.p)) +
-                    ((int64_t)t.b * d.sb + (int64_t)t.l * d.sl + h * a.row.D) * ES;
-          row_store<IO, V>(p + at.a * ES, g[i]);
-          row_store<IO, V>(p + at.b * ES, g[i] + V);
+        for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
+        const float inv = row_inverse(fmaf(group_sum(ss, a.row.group), a.c, a.eps));
+#pragma unroll
+        for (int e = 0; e < 2 * V; ++e) {
+          f[e] *= inv;                     // x r
+          dw[e] = fmaf(g[e], f[e], dw[e]);
+          g[e] *= w[e];
+          dot = fmaf(f[e], g[e], dot);
         }
+        dot = group_sum(dot, a.row.group) * a.c;
+#pragma unroll
+        for (int e = 0; e < 2 * V; ++e) g[e] = (g[e] - f[e] * dot) * inv;
       }
+      if (in_row && h < heads) {
+        if (!at_step.live) {
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) g[e] = 0.f;
+        }
+        char* p = const_cast<char*>(static_cast<const char*>(dx.p)) +
+                  ((int64_t)at_step.b * dx.sb + (int64_t)at_step.l * dx.sl) * ES +
+                  h * a.row.D * ES;
+        row_store<IO, V>(p + at.a * ES, g);
+        row_store<IO, V>(p + at.b * ES, g + V);
+      }
+      load(i);
+      advance(a, &at_step, steps, waves);
     }
   }
   if (!a.part) return;
   // the workgroup's sum, in a fixed order: the row groups of each wave, then
   // the waves in turn
-  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) {
-    for (int o = a.row.group; o < 64; o <<= 1) {
-      dwq[e] += __shfl_xor(dwq[e], o);
-      dwk[e] += __shfl_xor(dwk[e], o);
-    }
-  }
+  for (int e = 0; e < 2 * V; ++e)
+    for (int o = a.row.group; o < 64; o <<= 1) dw[e] += __shfl_xor(dw[e], o);
   for (int k = 0; k < kQkWaves; ++k) {
-    if (wv == k && lane < a.row.lanes) {
+    if (wave_id() == k && lane < a.row.lanes) {
 #pragma unroll
       for (int e = 0; e < 2 * V; ++e) {
         const int d = e < V ? at.a + e : at.b + e - V;
-        w[d] = k ? w[d] + dwq[e] : dwq[e];
-        w[kRowMaxD + d] = k ? w[kRowMaxD + d] + dwk[e] : dwk[e];
+        sum[d] = k ? sum[d] + dw[e] : dw[e];
       }
     }
     __syncthreads();
   }
-  for (int i = threadIdx.x; i < 2 * a.row.D; i += kQkThreads) {
-    const int which = i >= a.row.D, d = i - which * a.row.D;
-    a.part[(int64_t)blockIdx.x * 2 * a.row.D + i] = w[which * kRowMaxD + d];
-  }
+  for (int d = threadIdx.x; d < a.row.D; d += kQkThreads)
+    a.part[((int64_t)blockIdx.x * 2 + second) * a.row.D + d] = sum[d];
 }
 
 // Sum of the workgroups' parts, in a fixed order: 32 columns a workgroup, 32
@@ -363,7 +397,7 @@ __global__ __launch_bounds__(1024) void qk_weights_kernel(QkArgs a, int wgs) {
   }
   if (slice == 0 && col < 2 * a.row.D) {
     const int which = col >= a.row.D;
-    a.dw[which][col - which * a.row.D] = sum[0][threadIdx.x & 31];
+    (which ? a.dw[1] : a.dw[0])[col - which * a.row.D] = sum[0][threadIdx.x & 31];
   }
 }
 
@@ -375,7 +409,7 @@ int qk_backward_wgs(int64_t tokens) {
 template <bool PACKED>
 static hipError_t forward_as(const QkArgs& a, int io, hipStream_t s) {
   const int64_t tokens = (int64_t)a.B * a.L, wgs = (tokens + kQkWaves - 1) / kQkWaves;
-  const dim3 g((unsigned)(wgs < (1 << 22) ? wgs : 1 << 22)), t(kQkThreads);
+  const dim3 g((unsigned)(wgs < kQkWgs ? wgs : kQkWgs)), t(kQkThreads);
   if (io == IO_BF16) {
     if (a.row.V == 8) hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 8, PACKED>), g, t, 0, s, a);
     else if (a.row.V == 4)
@@ -394,7 +428,7 @@ hipError_t launch_qk_forward(const QkArgs& a, int io, bool packed, hipStream_t s
 
 template <bool PACKED>
 static hipError_t backward_as(const QkArgs& a, int io, hipStream_t s) {
-  const dim3 g(qk_backward_wgs((int64_t)a.B * a.L)), t(kQkThreads);
+  const dim3 g(qk_backward_wgs((int64_t)a.B * a.L), 2), t(kQkThreads);
   if (io == IO_BF16) {
     if (a.row.V == 8) hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 8, PACKED>), g, t, 0, s, a);
     else if (a.row.V == 4)
