@@ -259,15 +259,28 @@ gdn_status check_lrec(const gdn_lrec_problem* p, Lrec* s) {
   if (s->chunks * p->B > ((int64_t(1) << 32) - 1) / 512 / strips) return GDN_ERR_BAD_SHAPE;
   return GDN_OK;
 }
-int64_t lrec_chunk_bytes(const gdn_lrec_problem* p, const Lrec& s) {
-  return (s.chunks * p->B * p->C * 4 + 255) / 256 * 256;
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t lrec_enter_bytes(const gdn_lrec_problem* p, const Lrec& s) {
+  return round256(s.chunks * p->B * p->C * 4);
+}
+// The workspace of a pass over several chunks: the counter, the chunks' maps,
+// the groups' states (kLrecGroup chunks each).
+struct LrecScan {
+  int64_t agg, pre, bytes;   // offsets, total
+};
+LrecScan lrec_scan(const gdn_lrec_problem* p, const Lrec& s) {
+  LrecScan r{0, 0, 0};
+  if (s.chunks == 1) return r;
+  const int64_t bc = (int64_t)p->B * p->C;
+  r.agg = 256;
+  r.pre = r.agg + round256(s.chunks * bc * 8);
+  r.bytes = r.pre + round256((s.chunks / kLrecGroup) * bc * 4);
+  return r;
 }
 int64_t lrec_ws(const gdn_lrec_problem* p, const Lrec& s, int op) {
-  // the chunks' maps (A, H), and the entering states where no saved buffer
-  // is given
   if (op == GDN_OP_STEP) return 0;
-  if (op == GDN_OP_FORWARD && s.chunks == 1) return 0;
-  return 3 * lrec_chunk_bytes(p, s);
+  // the backward also keeps the entering states where no saved buffer is given
+  return lrec_scan(p, s).bytes + (op == GDN_OP_BACKWARD ? lrec_enter_bytes(p, s) : 0);
 }
 
 struct LrecUse {
@@ -286,7 +299,8 @@ int lrec_vec(const gdn_lrec_problem* p, int es, int most, const LrecUse* use, in
   return most;
 }
 
-void lrec_args(const gdn_lrec_problem* p, const Lrec& s, int vec, LrecArgs* a) {
+void lrec_args(const gdn_lrec_problem* p, const Lrec& s, int vec, void* workspace,
+               LrecArgs* a) {
   a->B = p->B;
   a->L = p->L;
   a->C = p->C;
@@ -298,31 +312,14 @@ void lrec_args(const gdn_lrec_problem* p, const Lrec& s, int vec, LrecArgs* a) {
   a->x_sl = p->x_stride[1];
   a->z_sb = p->gate_stride[0];
   a->z_sl = p->gate_stride[1];
-}
-
-gdn_status run_lrec_forward(const gdn_lrec_problem* p, const Lrec& s, const void* x,
-                            const void* gate, const int32_t* lengths, const float* state_in,
-                            void* o, float* state_out, void* saved, void* workspace,
-                            hipStream_t stream) {
-  const LrecUse use[] = {{x, p->x_stride}, {gate, p->gate_stride}, {o, nullptr}};
-  const int vec = lrec_vec(p, s.es, 4, use, 3);
-  LrecArgs a{};
-  lrec_args(p, s, vec, &a);
-  a.x = x;
-  a.z = gate;
-  a.len = lengths;
-  a.h0 = state_in;
-  a.o = o;
-  a.hT = state_out;
   if (s.chunks > 1) {
+    const LrecScan sc = lrec_scan(p, s);
     char* ws = static_cast<char*>(workspace);
-    const int64_t n = lrec_chunk_bytes(p, s);
-    a.compA = reinterpret_cast<float*>(ws);
-    a.compH = reinterpret_cast<float*>(ws + n);
-    a.enter = reinterpret_cast<float*>(ws + 2 * n);
+    a->ticket = reinterpret_cast<unsigned*>(ws);
+    a->agg = reinterpret_cast<uint64_t*>(ws + sc.agg);
+    a->pre = reinterpret_cast<uint32_t*>(ws + sc.pre);
+    a->ws_bytes = sc.bytes;
   }
-  if (saved) a.enter = static_cast<float*>(saved);
-  return hip_status(launch_lrec_forward(a, s.io, vec, stream));
 }
 
 }  // namespace
@@ -529,7 +526,7 @@ gdn_status gdn_lrec_saved_size(const gdn_lrec_problem* p, size_t* bytes) {
   Lrec s;
   gdn_status st = check_lrec(p, &s);
   if (st != GDN_OK) return st;
-  *bytes = (size_t)lrec_chunk_bytes(p, s);
+  *bytes = (size_t)lrec_enter_bytes(p, s);
   return GDN_OK;
 }
 
@@ -553,10 +550,21 @@ gdn_status gdn_lrec_forward(const gdn_lrec_problem* p, const void* x, const void
                         flat(lengths, (int64_t)p->B * 4),
                         flat(state_out == state_in ? nullptr : state_in, stb)};
   const Region outs[] = {flat(o, n * s.es), flat(state_out, stb),
-                         flat(saved, lrec_chunk_bytes(p, s)), flat(need ? workspace : nullptr, need)};
+                         flat(saved, lrec_enter_bytes(p, s)),
+                        flat(need ? workspace : nullptr, need)};
   if (any_meet(outs, 4, ins, 4)) return GDN_ERR_ALIASING;
-  return run_lrec_forward(p, s, x, gate, lengths, state_in, o, state_out, saved, workspace,
-                          static_cast<hipStream_t>(stream));
+  const LrecUse use[] = {{x, p->x_stride}, {gate, p->gate_stride}, {o, nullptr}};
+  const int vec = s.io == IO_BF16 ? lrec_vec(p, s.es, 2, use, 3) : 1;
+  LrecArgs a{};
+  lrec_args(p, s, vec, workspace, &a);
+  a.x = x;
+  a.z = gate;
+  a.len = lengths;
+  a.h0 = state_in;
+  a.o = o;
+  a.hT = state_out;
+  a.enter = static_cast<float*>(saved);
+  return hip_status(launch_lrec_forward(a, s.io, vec, false, static_cast<hipStream_t>(stream)));
 }
 
 gdn_status gdn_lrec_step(const gdn_lrec_problem* p, const void* x, const void* gate,
@@ -586,7 +594,7 @@ gdn_status gdn_lrec_backward(const gdn_lrec_problem* p, const void* x, const voi
     return GDN_ERR_MISALIGNED;
   if (workspace_bytes < (size_t)need) return GDN_ERR_WORKSPACE_TOO_SMALL;
   const int64_t n = (int64_t)p->B * p->L * p->C, stb = (int64_t)p->B * p->C * 4;
-  const int64_t cb = lrec_chunk_bytes(p, s);
+  const int64_t cb = lrec_enter_bytes(p, s);
   const Region ins[] = {strided(x, p->B, p->L, p->C, p->x_stride, s.es),
                         strided(gate, p->B, p->L, p->C, p->gate_stride, s.es),
                         flat(lengths, (int64_t)p->B * 4), flat(state_in, stb),
@@ -597,9 +605,9 @@ gdn_status gdn_lrec_backward(const gdn_lrec_problem* p, const void* x, const voi
   if (any_meet(outs, 4, ins, 7)) return GDN_ERR_ALIASING;
   const LrecUse use[] = {{x, p->x_stride},   {gate, p->gate_stride}, {d_o, nullptr},
                          {dx, p->dx_stride}, {dgate, p->dgate_stride}};
-  const int vec = lrec_vec(p, s.es, 2, use, 5);
+  const int vec = s.io == IO_BF16 ? lrec_vec(p, s.es, 2, use, 5) : 1;
   LrecArgs a{};
-  lrec_args(p, s, vec, &a);
+  lrec_args(p, s, vec, workspace, &a);
   a.x = x;
   a.z = gate;
   a.len = lengths;
@@ -613,13 +621,14 @@ gdn_status gdn_lrec_backward(const gdn_lrec_problem* p, const void* x, const voi
   a.dz_sb = p->dgate_stride[0];
   a.dz_sl = p->dgate_stride[1];
   a.dh0 = d_state_in;
-  char* ws = static_cast<char*>(workspace);
-  a.compA = reinterpret_cast<float*>(ws);
-  a.compH = reinterpret_cast<float*>(ws + cb);
-  a.enter = saved ? const_cast<float*>(static_cast<const float*>(saved))
-                  : reinterpret_cast<float*>(ws + 2 * cb);
-  return hip_status(
-      launch_lrec_backward(a, s.io, vec, saved != nullptr, static_cast<hipStream_t>(stream)));
+  if (saved) {
+    a.enter = const_cast<float*>(static_cast<const float*>(saved));
+  } else {
+    a.enter = reinterpret_cast<float*>(static_cast<char*>(workspace) + lrec_scan(p, s).bytes);
+    st = hip_status(launch_lrec_forward(a, s.io, vec, true, static_cast<hipStream_t>(stream)));
+    if (st != GDN_OK) return st;
+  }
+  return hip_status(launch_lrec_backward(a, s.io, vec, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

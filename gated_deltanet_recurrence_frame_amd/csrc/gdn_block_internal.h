@@ -73,14 +73,19 @@ struct LrecArgs {
   void* dz;
   int64_t dx_sb, dx_sl, dz_sb, dz_sl;
   float* dh0;
-  float* compA;          // [B, chunks, C]
-  float* compH;
+  // several chunks: the counter, the chunks' maps [chunks][B C] (A low, H
+  // high) and the states entering every group but the first [groups][B C]
+  unsigned* ticket;
+  uint64_t* agg;
+  uint32_t* pre;
+  int64_t ws_bytes;      // from the counter on
   int B, L, C, chunks, strips;
   int logits, complement;
 };
 
-// Tokens of a chunk of the recurrence.
+// Tokens of a chunk of the recurrence, chunks of a group.
 constexpr int kLrecChunk = 128;
+constexpr int kLrecGroup = 8;
 
 hipError_t launch_pack8(const PackArgs& a, int io, hipStream_t s);
 hipError_t launch_unpack8(const PackArgs& a, int io, hipStream_t s);
@@ -88,9 +93,9 @@ hipError_t launch_qk_forward(const QkArgs& a, int io, bool packed, hipStream_t s
 // Workgroups of the backward pass: rows of `part`.
 int qk_backward_wgs(int64_t tokens);
 hipError_t launch_qk_backward(const QkArgs& a, int io, bool packed, hipStream_t s);
-// vec: elements a lane takes of a row at once (1, 2 or 4)
-hipError_t launch_lrec_forward(const LrecArgs& a, int io, int vec, hipStream_t s);
-hipError_t launch_lrec_backward(const LrecArgs& a, int io, int vec, bool have_enter,
-                                hipStream_t s);
+// vec: elements a lane takes of a row at once (bf16: 1 or 2, fp32: 1).
+// states: form enter alone, no outputs.
+hipError_t launch_lrec_forward(const LrecArgs& a, int io, int vec, bool states, hipStream_t s);
+hipError_t launch_lrec_backward(const LrecArgs& a, int io, int vec, hipStream_t s);
 
 }  // namespace gdn

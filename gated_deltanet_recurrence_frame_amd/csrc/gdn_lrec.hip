@@ -2,56 +2,57 @@
 //   h_l = a_l h_{l-1} + u_l  (gdn_lrec_forward), and its gradient
 //   G_l = do_l + a_{l+1} G_{l+1}  (gdn_lrec_backward).
 //
-// The tokens are cut into chunks of kLrecChunk.  The map of a chunk on the
-// state entering it is affine, h -> A h + H with A = prod a and H the chunk
-// run from zero; a pass forms every chunk's (A, H), a second runs over the
-// chunks, a third runs every chunk from the state entering it.  A workgroup
-// takes one chunk of 64 VEC channels: its waves take kTokens tokens each and
-// keep them in registers, their maps meet in LDS.
+// The tokens are cut into chunks.  The map of a chunk on the state entering it
+// is affine, h -> A h + H with A = prod a and H the chunk run from zero.  A
+// workgroup takes one chunk of 64 VEC channels, reads it once and keeps it in
+// registers (kTokens tokens a wave); the waves' maps meet in LDS, the chunks'
+// in the workspace, and every chunk is then run from the state entering it:
+// one pass over the tensors.
+//
+// The state entering a chunk comes from the chunks before it, in groups of
+// kGroup: from the state entering the group (published by the group before it
+// once its own is known) and the maps of the group's earlier chunks
+// (published by each as soon as it has read its tokens).  So the serial part
+// is one hand-over a group, and every state is formed in one fixed order: the
+// same bits every time.  A published word carries its own flag: the workspace
+// is filled with ones first and no value published has that pattern, so a
+// relaxed load of the word either sees it whole or not yet, and no fence is
+// needed.  Workgroups draw their chunk from a counter, in order: a chunk waits
+// only for chunks whose workgroups have begun, and those for earlier ones
+// still, so every wait ends whatever the order of dispatch.
 #include "gdn_block_internal.h"
 
 namespace gdn {
 
-constexpr int kTokens = 16;                          // tokens of a wave
+constexpr int kTokens = 16;                 // tokens of a wave
+constexpr int kGroup = kLrecGroup;
 constexpr int kLrecWaves = kLrecChunk / kTokens;
 constexpr int kLrecThreads = 64 * kLrecWaves;
+static_assert(kGroup <= kLrecWaves, "a wave for each earlier chunk of a group and one for its state");
 
-// VEC io elements as loaded (bf16 in pairs), and as floats.
+// VEC io elements as loaded (bf16: one or two, fp32: one; a word either way),
+// and as floats.
 template <int IO, int VEC>
 struct Vec {
-  static constexpr int kWords = IO == IO_BF16 ? (VEC + 1) / 2 : VEC;
-  uint32_t u[kWords];
+  uint32_t u;
 
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) u[i] = 0u;
-  }
+  __device__ __forceinline__ void fill(uint32_t w) { u = w; }
   __device__ __forceinline__ void load(const void* p) {
-    if constexpr (IO == IO_BF16 && VEC == 1) u[0] = *reinterpret_cast<const uint16_t*>(p);
-    else if constexpr (kWords == 1) u[0] = *reinterpret_cast<const uint32_t*>(p);
-    else if constexpr (kWords == 2) *reinterpret_cast<u32x2*>(u) = *reinterpret_cast<const u32x2*>(p);
-    else *reinterpret_cast<u32x4*>(u) = *reinterpret_cast<const u32x4*>(p);
+    if constexpr (IO == IO_BF16 && VEC == 1) u = *reinterpret_cast<const uint16_t*>(p);
+    else u = *reinterpret_cast<const uint32_t*>(p);
   }
   __device__ __forceinline__ float get(int e) const {
-    if constexpr (IO == IO_F32) return __uint_as_float(u[e]);
-    else return __uint_as_float((e & 1) ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+    if constexpr (IO == IO_F32) return __uint_as_float(u);
+    else return __uint_as_float(e ? u & 0xffff0000u : u << 16);
   }
 };
 template <int IO, int VEC>
 __device__ __forceinline__ void vec_store(void* p, const float* f) {
-  if constexpr (IO == IO_BF16) {
-    uint32_t u[(VEC + 1) / 2];
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e)
-      u[e] = (uint32_t)f32_to_bf16_bits(f[2 * e]) | ((uint32_t)f32_to_bf16_bits(f[2 * e + 1]) << 16);
-    if constexpr (VEC == 4) *reinterpret_cast<u32x2*>(p) = u32x2{u[0], u[1]};
-    else if constexpr (VEC == 2) *reinterpret_cast<uint32_t*>(p) = u[0];
-    else *reinterpret_cast<uint16_t*>(p) = f32_to_bf16_bits(f[0]);
-  } else {
-    if constexpr (VEC == 4) *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
-    else if constexpr (VEC == 2) *reinterpret_cast<f32x2*>(p) = f32x2{f[0], f[1]};
-    else *reinterpret_cast<float*>(p) = f[0];
-  }
+  if constexpr (IO == IO_F32) *reinterpret_cast<float*>(p) = f[0];
+  else if constexpr (VEC == 2)
+    *reinterpret_cast<uint32_t*>(p) =
+        (uint32_t)f32_to_bf16_bits(f[0]) | ((uint32_t)f32_to_bf16_bits(f[1]) << 16);
+  else *reinterpret_cast<uint16_t*>(p) = f32_to_bf16_bits(f[0]);
 }
 
 // A gate is kept as one float from which a and 1 - a both come to full
@@ -85,9 +86,13 @@ __device__ __forceinline__ float gate_na(float v) {
   const float s = fabsf(v);
   return __float_as_int(v) < 0 ? 1.f - s : s;
 }
-// The gate that leaves the state as it is: a = 1, 1 - a = 0.
-template <bool LOGITS>
-__device__ __forceinline__ float gate_open() { return LOGITS ? 0.f : 1.f; }
+// A token behind the sequence's end leaves the state as it is: its gate as
+// loaded (a = 1, 1 - a = 0) and an input of 0.
+template <int IO, bool LOGITS>
+__device__ __forceinline__ uint32_t open_word() {
+  if constexpr (IO == IO_BF16) return LOGITS ? 0x7f807f80u : 0x3f803f80u;
+  return LOGITS ? 0x7f800000u : 0x3f800000u;
+}
 
 __device__ __forceinline__ int length_of(const LrecArgs& p, int b) {
   if (!p.len) return p.L;
@@ -97,224 +102,301 @@ __device__ __forceinline__ int length_of(const LrecArgs& p, int b) {
 
 // Where a workgroup and its wave stand.
 struct Tile {
-  int b, chunk, len;
-  int t0;          // the wave's first token
-  int c;           // the lane's first channel
-  bool in;         // below C
+  int b, step, chunk;   // step: the chunk's turn (backwards: from the end)
+  int t0, live;         // the wave's first token, its tokens before the sequence's end
+  int c0;               // the strip's first channel
+  int cl;               // the lane's first channel from there, of one that exists
+  bool in;              // the lane has channels of its own
 };
-template <int VEC>
+template <int VEC, bool REVERSE>
 __device__ __forceinline__ Tile tile_at(const LrecArgs& p) {
+  unsigned id = blockIdx.x;
+  if (p.chunks > 1) {
+    __shared__ unsigned drawn;
+    if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(drawn);
+  }
   Tile t;
   const unsigned per = (unsigned)p.B * p.strips;
-  t.chunk = blockIdx.x / per;
-  const unsigned r = blockIdx.x - t.chunk * per;
+  t.step = id / per;
+  t.chunk = REVERSE ? p.chunks - 1 - t.step : t.step;
+  const unsigned r = id - t.step * per;
   t.b = r / (unsigned)p.strips;
-  t.len = length_of(p, t.b);
   t.t0 = t.chunk * kLrecChunk + wave_id() * kTokens;
-  t.c = ((r - t.b * p.strips) * 64 + lane_id()) * VEC;
-  t.in = t.c < p.C;
+  t.live = length_of(p, t.b) - t.t0;
+  t.c0 = (r - t.b * p.strips) * 64 * VEC;
+  t.in = t.c0 + lane_id() * VEC < p.C;
+  t.cl = t.in ? lane_id() * VEC : 0;
   return t;
 }
 
-// The maps of the tile's waves, in LDS, [wave][64 VEC]: A and H.
+// Maps (A, H) of a chunk's waves or of a group's chunks, [index][64 VEC].
 template <int VEC>
 struct Maps {
   float A[kLrecWaves][64 * VEC], H[kLrecWaves][64 * VEC];
 };
 
-enum LrecMode { LREC_MAP = 0, LREC_RUN = 1 };
+constexpr uint32_t kUnset = 0xffffffffu;
+__device__ __forceinline__ uint32_t publishable(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return u == kUnset ? 0x7fc00000u : u;   // a NaN either way
+}
 
-// LREC_MAP: the chunk's (A, H) to compA, compH.  LREC_RUN: the outputs, from
-// enter[chunk] (h0 for the first chunk, whose enter is then written); the
-// last chunk writes hT.
-template <int IO, int VEC, bool LOGITS, int MODE>
+// The state entering the chunk, in h: `maps` holds the maps of the chunk's
+// waves (barrier passed), in the order `first`, `first + dir`, ...  `initial`
+// is the sequence's [B, C] or nullptr.
+template <int VEC, bool REVERSE>
+__device__ __forceinline__ void entering_state(const LrecArgs& p, const Tile& t,
+                                               const Maps<VEC>& maps, const float* initial,
+                                               float* h) {
+  const int w = wave_id(), col = lane_id() * VEC;
+  const int64_t BC = (int64_t)p.B * p.C, bc = (int64_t)t.b * p.C + t.c0 + t.cl;
+  if (p.chunks == 1) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) h[e] = initial ? initial[bc + e] : 0.f;
+    return;
+  }
+  __shared__ Maps<VEC> before;
+  __shared__ float start[64 * VEC];
+  const int g = t.step / kGroup, r = t.step % kGroup;
+  const bool last = t.step == p.chunks - 1;
+  if (w == 0 && t.in && r != kGroup - 1 && !last) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float A = 1.f, H = 0.f;
+#pragma unroll
+      for (int k = 0; k < kLrecWaves; ++k) {
+        const int v = REVERSE ? kLrecWaves - 1 - k : k;
+        H = fmaf(maps.A[v][col + e], H, maps.H[v][col + e]);
+        A *= maps.A[v][col + e];
+      }
+      __hip_atomic_store(p.agg + (int64_t)t.step * BC + bc + e,
+                         (uint64_t)publishable(A) | (uint64_t)__float_as_uint(H) << 32,
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (w < r) {
+    const uint64_t* from = p.agg + (int64_t)(t.step - r + w) * BC + bc;
+    uint64_t v[VEC];
+    bool there;
+    do {
+      there = true;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        v[e] = __hip_atomic_load(from + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        there = there && (uint32_t)v[e] != kUnset;
+      }
+    } while (!__all(there || !t.in));
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      before.A[w][col + e] = __uint_as_float((uint32_t)v[e]);
+      before.H[w][col + e] = __uint_as_float((uint32_t)(v[e] >> 32));
+    }
+  } else if (w == kLrecWaves - 1) {
+    if (g == 0) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) start[col + e] = initial ? initial[bc + e] : 0.f;
+    } else {
+      const uint32_t* from = p.pre + (int64_t)(g - 1) * BC + bc;
+      uint32_t v[VEC];
+      bool there;
+      do {
+        there = true;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          v[e] = __hip_atomic_load(from + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          there = there && v[e] != kUnset;
+        }
+      } while (!__all(there || !t.in));
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) start[col + e] = __uint_as_float(v[e]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) h[e] = start[col + e];
+  for (int k = 0; k < r; ++k)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) h[e] = fmaf(before.A[k][col + e], h[e], before.H[k][col + e]);
+  if (w == 0 && t.in && r == kGroup - 1 && !last) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float n = h[e];
+#pragma unroll
+      for (int k = 0; k < kLrecWaves; ++k) {
+        const int v = REVERSE ? kLrecWaves - 1 - k : k;
+        n = fmaf(maps.A[v][col + e], n, maps.H[v][col + e]);
+      }
+      __hip_atomic_store(p.pre + (int64_t)g * BC + bc + e, publishable(n), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+}
+
+// A tensor at the wave's first token and the strip's first channel: the same
+// for all lanes, so that an access is a scalar address and the lane's offset.
+template <int IO>
+__device__ __forceinline__ const char* wave_row(const Tile& t, const void* base, int64_t sb,
+                                                int64_t sl) {
+  return static_cast<const char*>(base) +
+         ((int64_t)t.b * sb + (int64_t)t.t0 * sl + t.c0) * Io<IO>::bytes;
+}
+template <int IO>
+__device__ __forceinline__ char* wave_row(const Tile& t, void* base, int64_t sb, int64_t sl) {
+  return const_cast<char*>(wave_row<IO>(t, static_cast<const void*>(base), sb, sl));
+}
+// Likewise of an fp32 [B, n, C] at (b, i).
+__device__ __forceinline__ float* state_row(const LrecArgs& p, const Tile& t, float* base, int n,
+                                            int i) {
+  return base + ((int64_t)t.b * n + i) * p.C + t.c0;
+}
+
+// The wave's tokens of one tensor, row by row at stride `sl` elements; rows
+// behind the sequence's end read its last row again (`dead` replaces what was
+// read), a wave without a row reads nothing.
+template <int IO, int VEC>
+__device__ __forceinline__ void load_tokens(const Tile& t, const void* base, int64_t sb,
+                                            int64_t sl, uint32_t dead, Vec<IO, VEC>* v) {
+  if (t.live <= 0) {
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) v[i].fill(dead);
+    return;
+  }
+  const char* row = wave_row<IO>(t, base, sb, sl);
+  const uint32_t off = t.cl * Io<IO>::bytes;
+  const int end = t.live - 1;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+    v[i].load(row + (i < end ? i : end) * sl * Io<IO>::bytes + off);
+  if (t.live < kTokens) {
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i)
+      if (i >= t.live) v[i].fill(dead);
+  }
+}
+
+// STATES: only the states entering the chunks (enter), else the outputs too.
+template <int IO, int VEC, bool LOGITS, bool STATES>
 __global__ __launch_bounds__(kLrecThreads) void lrec_forward_kernel(LrecArgs p) {
   constexpr int ES = Io<IO>::bytes;
   __shared__ Maps<VEC> maps;
-  const Tile t = tile_at<VEC>(p);
+  const Tile t = tile_at<VEC, false>(p);
   const int w = wave_id(), col = lane_id() * VEC;
-  const int live = t.len - t.t0;   // tokens of the wave before the sequence's end
-  Vec<IO, VEC> x[kTokens], z[kTokens];
-  float v[kTokens][VEC];
-  const char* xp = static_cast<const char*>(p.x) + (t.b * p.x_sb + t.t0 * p.x_sl + t.c) * ES;
-  const char* zp = static_cast<const char*>(p.z) + (t.b * p.z_sb + t.t0 * p.z_sl + t.c) * ES;
+  float a[kTokens][VEC], u[kTokens][VEC];
+  {
+    Vec<IO, VEC> x[kTokens], z[kTokens];
+    load_tokens<IO, VEC>(t, p.z, p.z_sb, p.z_sl, open_word<IO, LOGITS>(), z);
+    load_tokens<IO, VEC>(t, p.x, p.x_sb, p.x_sl, 0u, x);
+    float A[VEC], H[VEC];
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
-    x[i].clear();
-    z[i].clear();
-    if (t.in && i < live) {
-      x[i].load(xp + i * p.x_sl * ES);
-      z[i].load(zp + i * p.z_sl * ES);
+    for (int e = 0; e < VEC; ++e) A[e] = 1.f, H[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float v = gate_keep<IO, LOGITS>(z[i].get(e));
+        a[i][e] = gate_a<LOGITS>(v);
+        u[i][e] = x[i].get(e) * (p.complement ? gate_na<LOGITS>(v) : 1.f);
+        A[e] *= a[i][e];
+        H[e] = fmaf(a[i][e], H[e], u[i][e]);
+      }
     }
-  }
-  float A[VEC], H[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) A[e] = 1.f, H[e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      v[i][e] = i < live ? gate_keep<IO, LOGITS>(z[i].get(e)) : gate_open<LOGITS>();
-      const float a = gate_a<LOGITS>(v[i][e]);
-      const float u = x[i].get(e) * (p.complement ? gate_na<LOGITS>(v[i][e]) : 1.f);
-      A[e] *= a;
-      H[e] = fmaf(a, H[e], u);
+      maps.A[w][col + e] = A[e];
+      maps.H[w][col + e] = H[e];
     }
-  }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    maps.A[w][col + e] = A[e];
-    maps.H[w][col + e] = H[e];
   }
   __syncthreads();
-  if (!t.in) return;
-  const int64_t at = ((int64_t)t.b * p.chunks + t.chunk) * p.C + t.c;
-  if constexpr (MODE == LREC_MAP) {
-    if (w != 0) return;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float ca = maps.A[0][col + e], ch = maps.H[0][col + e];
-      for (int k = 1; k < kLrecWaves; ++k) {
-        ch = fmaf(maps.A[k][col + e], ch, maps.H[k][col + e]);
-        ca *= maps.A[k][col + e];
-      }
-      p.compA[at + e] = ca;
-      p.compH[at + e] = ch;
-    }
-    return;
-  }
-  const int64_t hc = (int64_t)t.b * p.C + t.c;
   float h[VEC];
+  entering_state<VEC, false>(p, t, maps, p.h0, h);
+  if (!t.in) return;
+  if (p.enter && w == 0) {
+    float* q = state_row(p, t, p.enter, p.chunks, t.chunk);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e)
-    h[e] = t.chunk == 0 ? (p.h0 ? p.h0[hc + e] : 0.f) : p.enter[at + e];
-  if (t.chunk == 0 && p.enter && w == 0) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) p.enter[at + e] = h[e];
+    for (int e = 0; e < VEC; ++e) q[t.cl + e] = h[e];
   }
-  for (int k = 0; k < w; ++k) {
+  if constexpr (STATES) return;
+  for (int k = 0; k < w; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) h[e] = fmaf(maps.A[k][col + e], h[e], maps.H[k][col + e]);
-  }
-  char* op = static_cast<char*>(p.o) + (((int64_t)t.b * p.L + t.t0) * p.C + t.c) * ES;
+  char* op = wave_row<IO>(t, p.o, (int64_t)p.L * p.C, p.C);
+  const uint32_t off = t.cl * ES;
+  const int rows = p.L - t.t0;
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     float o[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float u = x[i].get(e) * (p.complement ? gate_na<LOGITS>(v[i][e]) : 1.f);
-      h[e] = fmaf(gate_a<LOGITS>(v[i][e]), h[e], u);
-      o[e] = i < live ? h[e] : 0.f;
+      h[e] = fmaf(a[i][e], h[e], u[i][e]);
+      o[e] = i < t.live ? h[e] : 0.f;
     }
-    if (t.t0 + i < p.L) vec_store<IO, VEC>(op + (int64_t)i * p.C * ES, o);
+    if (i < rows) vec_store<IO, VEC>(op + (int64_t)i * p.C * ES + off, o);
   }
   if (p.hT && t.chunk == p.chunks - 1 && w == kLrecWaves - 1) {
+    float* q = state_row(p, t, p.hT, 1, 0);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) p.hT[hc + e] = h[e];
+    for (int e = 0; e < VEC; ++e) q[t.cl + e] = h[e];
   }
 }
 
-// The state entering every chunk, from the chunks' maps: forwards from h0
-// (enter), or backwards from dhT (the carry a_{l+1} G_{l+1} entering every
-// chunk from behind, in place of compH).
-template <bool REVERSE>
-__global__ __launch_bounds__(256) void lrec_carry_kernel(LrecArgs p) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)p.B * p.C) return;
-  const int64_t b = i / p.C, c = i - b * p.C, first = b * p.chunks * p.C + c;
-  if constexpr (!REVERSE) {
-    float h = p.h0 ? p.h0[i] : 0.f;
-    for (int k = 0; k < p.chunks; ++k) {
-      const int64_t at = first + (int64_t)k * p.C;
-      p.enter[at] = h;
-      h = fmaf(p.compA[at], h, p.compH[at]);
-    }
-  } else {
-    float g = p.dhT ? p.dhT[i] : 0.f;
-    for (int k = p.chunks - 1; k >= 0; --k) {
-      const int64_t at = first + (int64_t)k * p.C;
-      const float next = fmaf(p.compA[at], g, p.compH[at]);
-      p.compH[at] = g;
-      g = next;
-    }
-  }
-}
+// Makes a register's value unknown to the compiler: what was formed from it
+// is formed again after this rather than kept (the backward's gates in three
+// forms and unpacked rows would fill 250 registers, and with them a second
+// workgroup's place on the CU).
+__device__ __forceinline__ void formed_again(float& f) { asm volatile("" : "+v"(f)); }
+__device__ __forceinline__ void formed_again(uint32_t& u) { asm volatile("" : "+v"(u)); }
 
-// LREC_MAP: the chunk's map on the carry coming from behind.  LREC_RUN: the
-// gradients, from the carry in compH and the state in enter.
-template <int IO, int VEC, bool LOGITS, int MODE>
+// The gradients; the states entering the chunks are in enter.
+template <int IO, int VEC, bool LOGITS>
 __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p) {
   constexpr int ES = Io<IO>::bytes;
   __shared__ Maps<VEC> back, fore;
-  const Tile t = tile_at<VEC>(p);
+  const Tile t = tile_at<VEC, true>(p);
   const int w = wave_id(), col = lane_id() * VEC;
-  const int live = t.len - t.t0;
   Vec<IO, VEC> x[kTokens], d[kTokens];
   float v[kTokens][VEC];
-  const char* xp = static_cast<const char*>(p.x) + (t.b * p.x_sb + t.t0 * p.x_sl + t.c) * ES;
-  const char* zp = static_cast<const char*>(p.z) + (t.b * p.z_sb + t.t0 * p.z_sl + t.c) * ES;
-  const char* dp = static_cast<const char*>(p.d_o) + (((int64_t)t.b * p.L + t.t0) * p.C + t.c) * ES;
+  float h[VEC];
   {
     Vec<IO, VEC> z[kTokens];
+    load_tokens<IO, VEC>(t, p.z, p.z_sb, p.z_sl, open_word<IO, LOGITS>(), z);
+    load_tokens<IO, VEC>(t, p.d_o, (int64_t)p.L * p.C, p.C, 0u, d);
+    load_tokens<IO, VEC>(t, p.x, p.x_sb, p.x_sl, 0u, x);
+    const float* q = state_row(p, t, p.enter, p.chunks, t.chunk);
+    float A[VEC], H[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) h[e] = q[t.cl + e], A[e] = 1.f, H[e] = 0.f;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      x[i].clear();
-      z[i].clear();
-      d[i].clear();
-      if (t.in && i < live) {
-        z[i].load(zp + i * p.z_sl * ES);
-        d[i].load(dp + (int64_t)i * p.C * ES);
-        if constexpr (MODE == LREC_RUN) x[i].load(xp + i * p.x_sl * ES);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        v[i][e] = gate_keep<IO, LOGITS>(z[i].get(e));
+        const float a = gate_a<LOGITS>(v[i][e]);
+        A[e] *= a;
+        H[e] = fmaf(a, H[e], x[i].get(e) * (p.complement ? gate_na<LOGITS>(v[i][e]) : 1.f));
       }
     }
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        v[i][e] = i < live ? gate_keep<IO, LOGITS>(z[i].get(e)) : gate_open<LOGITS>();
-  }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    float A = 1.f, H = 0.f;
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      const float a = gate_a<LOGITS>(v[i][e]);
-      A *= a;
-      if constexpr (MODE == LREC_RUN)
-        H = fmaf(a, H, x[i].get(e) * (p.complement ? gate_na<LOGITS>(v[i][e]) : 1.f));
-    }
-    if constexpr (MODE == LREC_RUN) {
-      fore.A[w][col + e] = A;
-      fore.H[w][col + e] = H;
-    }
-    H = 0.f;
-#pragma unroll
-    for (int i = kTokens - 1; i >= 0; --i) H = gate_a<LOGITS>(v[i][e]) * (d[i].get(e) + H);
-    back.A[w][col + e] = A;
-    back.H[w][col + e] = H;
-  }
-  __syncthreads();
-  if (!t.in) return;
-  const int64_t at = ((int64_t)t.b * p.chunks + t.chunk) * p.C + t.c;
-  if constexpr (MODE == LREC_MAP) {
-    if (w != 0) return;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      float ca = 1.f, ch = 0.f;
-      for (int k = kLrecWaves - 1; k >= 0; --k) {
-        ch = fmaf(back.A[k][col + e], ch, back.H[k][col + e]);
-        ca *= back.A[k][col + e];
-      }
-      p.compA[at + e] = ca;
-      p.compH[at + e] = ch;
-    }
-    return;
-  }
-  float h[VEC], c[VEC];
+      float G = 0.f;
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    h[e] = p.enter[at + e];
-    c[e] = p.compH[at + e];
+      for (int i = kTokens - 1; i >= 0; --i) G = gate_a<LOGITS>(v[i][e]) * (d[i].get(e) + G);
+      fore.A[w][col + e] = back.A[w][col + e] = A[e];
+      fore.H[w][col + e] = H[e];
+      back.H[w][col + e] = G;
+    }
+  }
+  __syncthreads();
+  float c[VEC];
+  entering_state<VEC, true>(p, t, back, p.dhT, c);
+  if (!t.in) return;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    formed_again(x[i].u);
+    formed_again(d[i].u);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) formed_again(v[i][e]);
   }
   for (int k = 0; k < w; ++k)
 #pragma unroll
@@ -333,8 +415,14 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p)
                   xv * (p.complement ? gate_na<LOGITS>(v[i][e]) : 1.f));
     }
   }
-  char* dxp = static_cast<char*>(p.dx) + (t.b * p.dx_sb + t.t0 * p.dx_sl + t.c) * ES;
-  char* dzp = static_cast<char*>(p.dz) + (t.b * p.dz_sb + t.t0 * p.dz_sl + t.c) * ES;
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) formed_again(v[i][e]);
+  char* dxp = wave_row<IO>(t, p.dx, p.dx_sb, p.dx_sl);
+  char* dzp = wave_row<IO>(t, p.dz, p.dz_sb, p.dz_sl);
+  const uint32_t off = t.cl * ES;
+  const int rows = p.L - t.t0;
 #pragma unroll
   for (int i = kTokens - 1; i >= 0; --i) {
     float dx[VEC], dz[VEC];
@@ -343,72 +431,74 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p)
       const float a = gate_a<LOGITS>(v[i][e]), na = gate_na<LOGITS>(v[i][e]);
       const float G = d[i].get(e) + c[e];
       const float da = G * f[i][e];
-      dz[e] = i < live ? (LOGITS ? da * (a * na) : da) : 0.f;
-      dx[e] = i < live ? (p.complement ? G * na : G) : 0.f;
+      dz[e] = i < t.live ? (LOGITS ? da * (a * na) : da) : 0.f;
+      dx[e] = i < t.live ? (p.complement ? G * na : G) : 0.f;
       c[e] = a * G;
     }
-    if (t.t0 + i < p.L) {
-      vec_store<IO, VEC>(dxp + i * p.dx_sl * ES, dx);
-      vec_store<IO, VEC>(dzp + i * p.dz_sl * ES, dz);
+    if (i < rows) {
+      vec_store<IO, VEC>(dxp + i * p.dx_sl * ES + off, dx);
+      vec_store<IO, VEC>(dzp + i * p.dz_sl * ES + off, dz);
     }
   }
   if (p.dh0 && t.chunk == 0 && w == 0) {
+    float* q = state_row(p, t, p.dh0, 1, 0);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) p.dh0[(int64_t)t.b * p.C + t.c + e] = c[e];
+    for (int e = 0; e < VEC; ++e) q[t.cl + e] = c[e];
   }
 }
 
-template <int IO, int VEC, bool LOGITS>
-static hipError_t forward_as(const LrecArgs& p, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(kLrecThreads);
-  const dim3 gc((unsigned)(((int64_t)p.B * p.C + 255) / 256));
-  if (p.chunks > 1) {
-    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, LREC_MAP>), g, t, 0, s, p);
-    hipLaunchKernelGGL((lrec_carry_kernel<false>), gc, dim3(256), 0, s, p);
+// The workspace before a pass over several chunks: words not yet published,
+// and the counter (its first 16 bytes) at 0.
+__global__ __launch_bounds__(256) void lrec_clear_kernel(u32x4* ws, int64_t n) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (; i < n; i += (int64_t)gridDim.x * 256) {
+    const uint32_t v = i == 0 ? 0u : kUnset;
+    ws[i] = u32x4{v, v, v, v};
   }
-  hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, LREC_RUN>), g, t, 0, s, p);
+}
+
+static void clear(const LrecArgs& p, hipStream_t s) {
+  const int64_t n = p.ws_bytes / 16, wgs = (n + 255) / 256;
+  hipLaunchKernelGGL(lrec_clear_kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, s,
+                     reinterpret_cast<u32x4*>(p.ticket), n);
+}
+
+template <int IO, int VEC, bool LOGITS>
+static hipError_t forward_as(const LrecArgs& p, bool states, hipStream_t s) {
+  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(kLrecThreads);
+  if (p.chunks > 1) clear(p, s);
+  if (states) hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, true>), g, t, 0, s, p);
+  else hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, false>), g, t, 0, s, p);
   return hipGetLastError();
 }
 
 template <int IO, int VEC, bool LOGITS>
-static hipError_t backward_as(const LrecArgs& p, bool have_enter, hipStream_t s) {
+static hipError_t backward_as(const LrecArgs& p, hipStream_t s) {
   const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(kLrecThreads);
-  const dim3 gc((unsigned)(((int64_t)p.B * p.C + 255) / 256));
-  if (!have_enter) {
-    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, LREC_MAP>), g, t, 0, s, p);
-    hipLaunchKernelGGL((lrec_carry_kernel<false>), gc, dim3(256), 0, s, p);
-  }
-  hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, LOGITS, LREC_MAP>), g, t, 0, s, p);
-  hipLaunchKernelGGL((lrec_carry_kernel<true>), gc, dim3(256), 0, s, p);
-  hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, LOGITS, LREC_RUN>), g, t, 0, s, p);
+  if (p.chunks > 1) clear(p, s);
+  hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, LOGITS>), g, t, 0, s, p);
   return hipGetLastError();
 }
 
-hipError_t launch_lrec_forward(const LrecArgs& p, int io, int vec, hipStream_t s) {
-  if (io == IO_BF16) {
-    if (vec == 4)
-      return p.logits ? forward_as<IO_BF16, 4, true>(p, s) : forward_as<IO_BF16, 4, false>(p, s);
-    return p.logits ? forward_as<IO_BF16, 1, true>(p, s) : forward_as<IO_BF16, 1, false>(p, s);
-  }
-  if (vec == 4)
-    return p.logits ? forward_as<IO_F32, 4, true>(p, s) : forward_as<IO_F32, 4, false>(p, s);
-  return p.logits ? forward_as<IO_F32, 1, true>(p, s) : forward_as<IO_F32, 1, false>(p, s);
-}
-
-hipError_t launch_lrec_backward(const LrecArgs& p, int io, int vec, bool have_enter,
-                                hipStream_t s) {
+hipError_t launch_lrec_forward(const LrecArgs& p, int io, int vec, bool states, hipStream_t s) {
   if (io == IO_BF16) {
     if (vec == 2)
-      return p.logits ? backward_as<IO_BF16, 2, true>(p, have_enter, s)
-                      : backward_as<IO_BF16, 2, false>(p, have_enter, s);
-    return p.logits ? backward_as<IO_BF16, 1, true>(p, have_enter, s)
-                    : backward_as<IO_BF16, 1, false>(p, have_enter, s);
+      return p.logits ? forward_as<IO_BF16, 2, true>(p, states, s)
+                      : forward_as<IO_BF16, 2, false>(p, states, s);
+    return p.logits ? forward_as<IO_BF16, 1, true>(p, states, s)
+                    : forward_as<IO_BF16, 1, false>(p, states, s);
   }
-  if (vec == 2)
-    return p.logits ? backward_as<IO_F32, 2, true>(p, have_enter, s)
-                    : backward_as<IO_F32, 2, false>(p, have_enter, s);
-  return p.logits ? backward_as<IO_F32, 1, true>(p, have_enter, s)
-                  : backward_as<IO_F32, 1, false>(p, have_enter, s);
+  return p.logits ? forward_as<IO_F32, 1, true>(p, states, s)
+                  : forward_as<IO_F32, 1, false>(p, states, s);
+}
+
+hipError_t launch_lrec_backward(const LrecArgs& p, int io, int vec, hipStream_t s) {
+  if (io == IO_BF16) {
+    if (vec == 2)
+      return p.logits ? backward_as<IO_BF16, 2, true>(p, s) : backward_as<IO_BF16, 2, false>(p, s);
+    return p.logits ? backward_as<IO_BF16, 1, true>(p, s) : backward_as<IO_BF16, 1, false>(p, s);
+  }
+  return p.logits ? backward_as<IO_F32, 1, true>(p, s) : backward_as<IO_F32, 1, false>(p, s);
 }
 
 }  // namespace gdn
