@@ -154,6 +154,8 @@ gdn_status pack_args(const gdn_pack8_problem* p, const Pack& s, const void* x,
   a->B = p->B;
   a->L = p->L;
   a->H = p->H;
+  const int64_t w = (int64_t)p->H * p->D;
+  a->linear = (p->L == 1 || p->stride[1] == w) && (p->B == 1 || p->stride[0] == p->L * w);
   return GDN_OK;
 }
 
@@ -431,7 +433,7 @@ gdn_status gdn_qk_workspace_size(const gdn_qk_problem* p, int want_weights, size
   gdn_status st = check_qk(p, &s);
   if (st != GDN_OK) return st;
   *bytes = want_weights
-               ? (size_t)qk_backward_wgs((int64_t)p->B * p->L) * 2 * p->D * sizeof(float)
+               ? (size_t)(qk_backward_parts((int64_t)p->B * p->L) * p->D * 4)
                : 0;
   return GDN_OK;
 }
@@ -460,7 +462,7 @@ gdn_status gdn_qk_backward(const gdn_qk_problem* p, const void* q, const void* k
       !aligned(workspace, 16))
     return GDN_ERR_MISALIGNED;
   const int64_t need =
-      dq_weight ? (int64_t)qk_backward_wgs((int64_t)p->B * p->L) * 2 * p->D * 4 : 0;
+      dq_weight ? qk_backward_parts((int64_t)p->B * p->L) * p->D * 4 : 0;
   if (need && workspace_bytes < (size_t)need) return GDN_ERR_WORKSPACE_TOO_SMALL;
   QkArgs a{};
   qk_args(p, s, &a);

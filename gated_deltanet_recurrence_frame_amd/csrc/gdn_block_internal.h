@@ -34,6 +34,7 @@ struct PackArgs {
   void* scale;     // [B, L, H] uint8
   int B, L, H;
   RowShape row;
+  bool linear;     // x is contiguous
 };
 
 struct QkArgs {
@@ -47,11 +48,12 @@ struct QkArgs {
   uint8_t* v8_out[2];      // forward: checkpoints written, or nullptr
   uint8_t* s8_out[2];
   RowView dx[2];           // backward: gradients
-  float* part;             // backward: per-workgroup weight gradients [wgs][2][D]
+  float* part;             // backward: the workgroups' sums for dw [wgs][D]
   float* dw[2];
   int B, L, H[2];
   RowShape row;
   int norm, adjacent, axes, pairs, bound1, bound2;   // pairs of axes 0, of 0 and 1
+  int split;               // workgroups on the first operand, the rest on the second
   int pos_shared;
   float eps, c;
   // turns (angle / 2 pi) per unit of position of every pair
@@ -90,8 +92,8 @@ constexpr int kLrecGroup = 8;
 hipError_t launch_pack8(const PackArgs& a, int io, hipStream_t s);
 hipError_t launch_unpack8(const PackArgs& a, int io, hipStream_t s);
 hipError_t launch_qk_forward(const QkArgs& a, int io, bool packed, hipStream_t s);
-// Workgroups of the backward pass: rows of `part`.
-int qk_backward_wgs(int64_t tokens);
+// Workgroups of the backward pass at most: rows of `part`.
+int64_t qk_backward_parts(int64_t tokens);
 hipError_t launch_qk_backward(const QkArgs& a, int io, bool packed, hipStream_t s);
 // vec: elements a lane takes of a row at once (bf16: 1 or 2, fp32: 1).
 // states: form enter alone, no outputs.

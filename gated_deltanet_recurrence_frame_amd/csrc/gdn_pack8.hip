@@ -14,6 +14,7 @@ constexpr int kPackRows = 4;    // rows of a lane in flight
 // Row r (of B L H) of the strided tensor.
 template <int IO>
 __device__ __forceinline__ const char* io_row(const PackArgs& a, uint32_t r) {
+  if (a.linear) return static_cast<const char*>(a.x.p) + (int64_t)r * a.row.D * Io<IO>::bytes;
   const uint32_t tok = r / (uint32_t)a.H, h = r - tok * (uint32_t)a.H;
   const uint32_t b = tok / (uint32_t)a.L, l = tok - b * (uint32_t)a.L;
   return static_cast<const char*>(a.x.p) +
@@ -22,34 +23,27 @@ __device__ __forceinline__ const char* io_row(const PackArgs& a, uint32_t r) {
 
 template <int IO, int V>
 __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
+  constexpr int ES = Io<IO>::bytes;
   const int rpw = 64 / a.row.group;
   const uint32_t rows = (uint32_t)a.B * a.L * a.H;
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const bool in_row = j < a.row.lanes;
   const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
-  const Slot at = {2 * j * V, 2 * j * V + V};
+  const uint32_t at = in_row ? 2 * j * V : 0;   // a lane without a piece reads the row's first
   IoRow<IO, V> x[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
-    x[i].clear();
-    if (in_row && r < rows) x[i].load(io_row<IO>(a, r), at);
+    x[i].load(io_row<IO>(a, r < rows ? r : rows - 1), at * ES, (at + V) * ES);
   }
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
     const int s = scale_byte(group_max(row_max<IO, V>(x[i]), a.row.group));
-    const float m = pack_factor(s);
-    float f[2 * V];
-    x[i].get(f);
-#pragma unroll
-    for (int e = 0; e < 2 * V; ++e) f[e] *= m;
+    E4m3Row<V> v;
+    v.set(x[i], s);
     if (r < rows) {
-      if (in_row) {
-        uint8_t* v = static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D;
-        e4m3_store<V>(v + at.a, f);
-        e4m3_store<V>(v + at.b, f + V);
-      }
+      if (in_row) v.store(static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D, at, at + V);
       if (j == 0) static_cast<uint8_t*>(a.scale)[r] = (uint8_t)s;
     }
   }
@@ -57,33 +51,29 @@ __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
 
 template <int IO, int V>
 __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
+  constexpr int ES = Io<IO>::bytes;
   const int rpw = 64 / a.row.group;
   const uint32_t rows = (uint32_t)a.B * a.L * a.H;
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
   if (j >= a.row.lanes) return;
-  const Slot at = {2 * j * V, 2 * j * V + V};
+  const uint32_t at = 2 * j * V;
   E4m3Row<V> v[kPackRows];
-  float m[kPackRows];
+  int s[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
-    const uint32_t r = base + i * rpw;
-    if (r < rows) {
-      v[i].load(static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D, at);
-      m[i] = unpack_factor(static_cast<const uint8_t*>(a.scale)[r]);
-    }
+    uint32_t r = base + i * rpw;
+    r = r < rows ? r : rows - 1;
+    v[i].load(static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D, at, at + V);
+    s[i] = static_cast<const uint8_t*>(a.scale)[r];
   }
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
     if (r < rows) {
-      float f[2 * V];
-      v[i].get(f);
-#pragma unroll
-      for (int e = 0; e < 2 * V; ++e) f[e] *= m[i];
-      char* p = const_cast<char*>(io_row<IO>(a, r));
-      row_store<IO, V>(p + at.a * Io<IO>::bytes, f);
-      row_store<IO, V>(p + at.b * Io<IO>::bytes, f + V);
+      IoRow<IO, V> x;
+      v[i].get(&x, s[i]);
+      x.store(const_cast<char*>(io_row<IO>(a, r)), at * ES, (at + V) * ES);
     }
   }
 }

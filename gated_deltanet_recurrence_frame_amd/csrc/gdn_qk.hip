@@ -1,27 +1,35 @@
 // Queries and keys of a projection: norm per head and rotation by position
 // in one pass (gdn_qk_forward), and its gradient (gdn_qk_backward).
 //
-// A wave takes one token after the other: the rows of its heads lie next to
-// each other over groups of lanes (RowShape), 64 / group rows a step.  The rotation's
-// cosines and sines are the same for every head of a token, so the wave's
-// lanes form one pair's each, once a token (the angle in turns in 64 bits,
-// reduced to (-1/2, 1/2] before it is rounded), and pass them through LDS;
-// the two members of a pair are in one lane (row_slot), so the rotation
-// itself moves nothing between lanes.  Bytes alone bound both passes.
+// A workgroup is on one operand (its pointers, weights and their gradients'
+// sums are then one set of registers); the workgroups are shared out by the
+// operands' rows.  A wave takes one token after the other: the rows of its
+// heads lie next to each other over groups of lanes (RowShape), 64 / group
+// heads a step, and are loaded kAhead steps before they are used.  The
+// rotation's cosines and sines are the same for every head of a token, so the
+// wave's lanes form one pair's each, once a token (the angle in turns in 64
+// bits, reduced to [-1/2, 1/2] before it is rounded; the hardware's sine and
+// cosine of turns are then within 2.1 2^-24, measured over that range), and
+// pass them through LDS; the two members of a pair are in one lane
+// (row_slot), so the rotation itself moves nothing between lanes.
 #include "gdn_rows.h"
 
 namespace gdn {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkWaves = kQkThreads / 64;
-constexpr int kQkAhead = 4;         // steps loaded ahead (forward)
-constexpr int kQkBackAhead = 3;     // (backward)
-constexpr int kQkWgs = 1024;        // workgroups of the forward pass at most
-constexpr int kQkBackWgs = 512;     // of the backward pass, for each operand
+constexpr int kAhead = 4;           // steps loaded ahead (forward)
+constexpr int kBackAhead = 3;       // (backward)
+// Workgroups at most: as many as the card holds at once (256 CUs, 4 SIMDs
+// with one wave of a workgroup each) at the waves a SIMD that the registers
+// are bounded for; one more would run alone at the end.
+constexpr int kWavesPerSimd = 4, kBackWavesPerSimd = 3;
+constexpr int kQkWgs = 256 * kWavesPerSimd;
+constexpr int kQkBackWgs = 256 * kBackWavesPerSimd;
 constexpr int kMaxPairs = kRowMaxD / 2;
 
-// Where a wave stands: a token, and a step of its rows (64 / group heads of
-// one operand).  The same for all lanes.
+// Where a wave stands: a token, and a step of its rows.  The same for all
+// lanes.
 struct Cursor {
   uint32_t tok, b, l;
   int step;
@@ -69,8 +77,13 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The token's cosines and sines, through LDS to the lanes' V pairs each:
-// trig[2 m], trig[2 m + 1] of pair m.
+// trig[2 m], trig[2 m + 1]: cosine and sine of pair m; (1, 0) behind the last
+// pair, for the elements that are not turned.
+__device__ __forceinline__ void trig_init(float* trig) {
+#pragma unroll
+  for (int i = 0; i < 2 * kMaxPairs / 64; ++i)
+    trig[lane_id() + 64 * i] = (lane_id() & 1) ? 0.f : 1.f;
+}
 template <int V>
 __device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, float* trig, int j,
                                             float* c, float* s) {
@@ -81,284 +94,289 @@ __device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, flo
     if (m < a.pairs) {
       double turn = (double)t.pos[i] * t.per[i];
       turn -= rint(turn);
-      float sn, cs;
-      sincospif(2.f * (float)turn, &sn, &cs);
-      trig[2 * m] = cs;
-      trig[2 * m + 1] = sn;
+      *reinterpret_cast<f32x2*>(trig + 2 * m) =
+          f32x2{__builtin_amdgcn_cosf((float)turn), __builtin_amdgcn_sinf((float)turn)};
     }
   }
   wave_lds_sync();
-  const bool turned = j * V < a.pairs;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    c[e] = turned ? trig[2 * (j * V + e)] : 1.f;
-    s[e] = turned ? trig[2 * (j * V + e) + 1] : 0.f;
+  for (int e = 0; e < V; e += 2) {
+    const f32x4 q = *reinterpret_cast<const f32x4*>(trig + 2 * (j * V + e));
+    c[e] = q[0];
+    s[e] = q[1];
+    c[e + 1] = q[2];
+    s[e + 1] = q[3];
   }
 }
 
 // Turn a lane's V pairs by phi (SIGN 1) or -phi (SIGN -1).
 template <int V, int SIGN>
-__device__ __forceinline__ void turn(float* f, const float* c, const float* s, bool adjacent) {
-  if (adjacent) {
+__device__ __forceinline__ void turn(float* f, const float* c, const float* s) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = f[2 * e], y = f[2 * e + 1], sn = SIGN * s[e];
-      f[2 * e] = x * c[e] - y * sn;
-      f[2 * e + 1] = x * sn + y * c[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = f[e], y = f[e + V], sn = SIGN * s[e];
-      f[e] = x * c[e] - y * sn;
-      f[e + V] = x * sn + y * c[e];
-    }
+  for (int e = 0; e < V; ++e) {
+    const float x = f[e], y = f[e + V], sn = SIGN * s[e];
+    f[e] = x * c[e] - y * sn;
+    f[e + V] = x * sn + y * c[e];
   }
 }
 
-// 1 / sqrt of a row's argument; 0 where that is 0, NaN stays.
+// 1 / sqrt of a row's argument (to 1.6 2^-24, measured); 0 where that is 0,
+// NaN stays.
 __device__ __forceinline__ float row_inverse(float ss) {
-  return ss > 0.f ? 1.f / sqrtf(ss) : ss;
+  return ss > 0.f ? __builtin_amdgcn_rsqf(ss) : ss;
 }
 
-// The operands' weights side by side: [2][kRowMaxD], 1 where there are none.
-__device__ __forceinline__ void stage_weights(const QkArgs& a, float* w) {
-  for (int i = threadIdx.x; i < 2 * a.row.D; i += kQkThreads) {
-    const int which = i >= a.row.D, d = i - which * a.row.D;
-    const float* p = which ? a.w[1] : a.w[0];
-    w[which * kRowMaxD + d] = p ? p[d] : 1.f;
+// What a workgroup is on: an operand, and how its lanes lie over the rows.
+template <int V, bool ADJACENT>
+struct Place {
+  bool second;
+  int heads, steps;
+  uint32_t first, waves;   // the wave's first token, the operand's waves
+  int j, rg, rpw;
+  bool in_row;
+  Slot at;
+
+  __device__ __forceinline__ explicit Place(const QkArgs& a) {
+    second = (int)blockIdx.x >= a.split;
+    const uint32_t wg = blockIdx.x - (second ? a.split : 0);
+    const uint32_t wgs = second ? gridDim.x - a.split : a.split;
+    first = wg * kQkWaves + wave_id();
+    waves = wgs * kQkWaves;
+    heads = second ? a.H[1] : a.H[0];
+    j = lane_id() & (a.row.group - 1);
+    rg = lane_id() / a.row.group;
+    rpw = 64 / a.row.group;
+    steps = (heads + rpw - 1) / rpw;
+    in_row = j < a.row.lanes;
+    at = row_slot<V, ADJACENT>(in_row ? j : 0, a.pairs);   // others read the first piece
   }
-  __syncthreads();
-}
+  // the lane's row in a step, or the step's last (read, not written)
+  __device__ __forceinline__ uint32_t row_of(int step) const {
+    const int left = heads - step * rpw - 1;
+    return rg < left ? rg : left;
+  }
+  __device__ __forceinline__ bool writes(int step) const {
+    return in_row && rg < heads - step * rpw;
+  }
+  // the lane's weights (1 without), in the order of its floats
+  __device__ __forceinline__ void weights(const QkArgs& a, float* w) const {
+    const float* p = second ? a.w[1] : a.w[0];
+#pragma unroll
+    for (int m = 0; m < 2 * V; ++m)
+      w[pair_place<V, ADJACENT>(m)] = p ? p[m < V ? at.a + m : at.b + m - V] : 1.f;
+  }
+};
 
 template <int IO, int V, bool PACKED> struct Source { typedef IoRow<IO, V> row; };
 template <int IO, int V> struct Source<IO, V, true> { typedef E4m3Row<V> row; };
 
-// Rows are loaded kQkAhead steps before they are used.
-template <int IO, int V, bool PACKED>
-__global__ __launch_bounds__(kQkThreads) void qk_forward_kernel(QkArgs a) {
-  __shared__ float trig_all[kQkWaves][2 * kMaxPairs];
-  __shared__ float w[2 * kRowMaxD];
+template <int IO, int V, bool PACKED, bool ADJACENT>
+__global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(QkArgs a) {
+  __shared__ __align__(16) float trig_all[kQkWaves][2 * kMaxPairs];
   constexpr int ES = Io<IO>::bytes;
-  const bool weighted = a.w[0] || a.w[1];
-  if (weighted) stage_weights(a, w);
-  const int lane = lane_id(), j = lane & (a.row.group - 1);
-  const int rg = lane / a.row.group, rpw = 64 / a.row.group;
-  const bool in_row = j < a.row.lanes;
-  const Slot at = row_slot<V>(j, a.pairs, a.adjacent);
-  const uint32_t tokens = (uint32_t)a.B * a.L, waves = gridDim.x * kQkWaves;
-  const int nq = (a.H[0] + rpw - 1) / rpw, steps = nq + (a.H[1] + rpw - 1) / rpw;
+  const Place<V, ADJACENT> pl(a);
+  const int D = a.row.D;
+  const uint32_t tokens = (uint32_t)a.B * a.L;
+  const RowView x = pl.second ? a.x[1] : a.x[0];
+  const uint8_t* v8 = pl.second ? a.v8[1] : a.v8[0];
+  const uint8_t* s8 = pl.second ? a.s8[1] : a.s8[0];
+  uint8_t* v8_out = pl.second ? a.v8_out[1] : a.v8_out[0];
+  uint8_t* s8_out = pl.second ? a.s8_out[1] : a.s8_out[0];
+  char* y = static_cast<char*>(pl.second ? a.y[1] : a.y[0]);
   float* trig = trig_all[wave_id()];
+  float w[2 * V], c[V], s[V];
+  pl.weights(a, w);
 
-  typename Source<IO, V, PACKED>::row ahead[kQkAhead];
-  int scale[kQkAhead];
-  Cursor ld, at_step;
+  typename Source<IO, V, PACKED>::row ahead[kAhead];
+  int scale[kAhead];
+  Cursor ld, cur;
   Turns turns;
-  set_token(a, &ld, blockIdx.x * kQkWaves + wave_id());
-  at_step = ld;
+  set_token(a, &ld, pl.first);
+  cur = ld;
+  trig_init(trig);
   if (a.pairs) {
     turns_init(a, &turns);
     turns_fetch(a, &turns, ld.tok);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) c[e] = 1.f, s[e] = 0.f;
   }
   auto load = [&](int i) {
-    const bool second = ld.step >= nq;
-    const int h = (ld.step - (second ? nq : 0)) * rpw + rg, heads = second ? a.H[1] : a.H[0];
-    ahead[i].clear();
-    scale[i] = 0;
-    if (in_row && h < heads && ld.tok < tokens && ld.live) {
+    if (ld.tok < tokens && ld.live) {
+      const uint32_t off = pl.row_of(ld.step) * D;
       if constexpr (PACKED) {
-        const int64_t row = (int64_t)ld.tok * heads + h;
-        ahead[i].load((second ? a.v8[1] : a.v8[0]) + row * a.row.D, at);
-        scale[i] = (second ? a.s8[1] : a.s8[0])[row];
+        const int64_t row = (int64_t)ld.tok * pl.heads + ld.step * pl.rpw;
+        ahead[i].load(v8 + row * D, off + pl.at.a, off + pl.at.b);
+        scale[i] = (s8 + row)[pl.row_of(ld.step)];
       } else {
-        const RowView& x = second ? a.x[1] : a.x[0];
-        ahead[i].load(static_cast<const char*>(x.p) +
-                          ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl) * ES +
-                          h * a.row.D * ES,
-                      at);
+        const char* p = static_cast<const char*>(x.p) +
+                        ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl + ld.step * pl.rpw * D) * ES;
+        ahead[i].load(p, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
       }
     }
-    advance(a, &ld, steps, waves);
+    advance(a, &ld, pl.steps, pl.waves);
   };
 #pragma unroll
-  for (int i = 0; i < kQkAhead; ++i) load(i);
+  for (int i = 0; i < kAhead; ++i) load(i);
 
-  float c[V], s[V];
-  while (at_step.tok < tokens) {
+  while (cur.tok < tokens) {
 #pragma unroll
-    for (int i = 0; i < kQkAhead; ++i) {
-      if (at_step.tok >= tokens) break;
-      if (at_step.step == 0 && a.pairs) {
-        token_turns<V>(a, turns, trig, j, c, s);
-        turns_fetch(a, &turns, at_step.tok + waves);
-      }
-      const bool second = at_step.step >= nq;
-      const int h = (at_step.step - (second ? nq : 0)) * rpw + rg;
-      const int heads = second ? a.H[1] : a.H[0];
-      const bool put = in_row && h < heads;
-      const int64_t row = (int64_t)at_step.tok * heads + h;
-      float f[2 * V];
-      ahead[i].get(f);
-      if constexpr (PACKED) {
-        const float m = unpack_factor(scale[i]);
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) f[e] *= m;
-      } else if (a.v8_out[0]) {
-        const int sb = scale_byte(group_max(row_max<IO, V>(ahead[i]), a.row.group));
-        const float k = pack_factor(sb);
-        float g[2 * V];
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) g[e] = f[e] * k;
-        if (put) {
-          uint8_t* v = (second ? a.v8_out[1] : a.v8_out[0]) + row * a.row.D;
-          e4m3_store<V>(v + at.a, g);
-          e4m3_store<V>(v + at.b, g + V);
-          if (j == 0) (second ? a.s8_out[1] : a.s8_out[0])[row] = (uint8_t)sb;
+    for (int i = 0; i < kAhead; ++i) {
+      if (cur.tok >= tokens) break;
+      const int64_t row = (int64_t)cur.tok * pl.heads + cur.step * pl.rpw;
+      const bool put = pl.writes(cur.step);
+      const uint32_t off = pl.rg * D;
+      IoRow<IO, V> out;
+      if (cur.live) {
+        if (cur.step == 0 && a.pairs) {
+          token_turns<V>(a, turns, trig, pl.j, c, s);
+          turns_fetch(a, &turns, cur.tok + pl.waves);
         }
-      }
-      if (a.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
-        const float inv = row_inverse(fmaf(group_sum(ss, a.row.group), a.c, a.eps));
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) f[e] *= inv;
-        if (weighted && in_row) {
-          const float* wv = w + (second ? kRowMaxD : 0);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            f[e] *= wv[at.a + e];
-            f[e + V] *= wv[at.b + e];
+        float f[2 * V], ss = 0.f;
+        if constexpr (PACKED) {
+          ahead[i].template get<ADJACENT>(f, scale[i]);
+        } else {
+          ahead[i].template get<ADJACENT>(f);
+          if (v8_out) {
+            const int sb = scale_byte(group_max(row_max<IO, V>(ahead[i]), a.row.group));
+            E4m3Row<V> v;
+            v.set(ahead[i], sb);
+            if (put) {
+              v.store(v8_out + row * D, off + pl.at.a, off + pl.at.b);
+              if (pl.j == 0) (s8_out + row)[pl.rg] = (uint8_t)sb;
+            }
           }
         }
-      }
-      if (a.pairs) turn<V, 1>(f, c, s, a.adjacent);
-      if (put) {
-        if (!at_step.live) {
+        if (a.norm) {
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e) f[e] = 0.f;
+          for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
+          ss = group_sum(pl.in_row ? ss : 0.f, a.row.group);
+          const float inv = row_inverse(fmaf(ss, a.c, a.eps));
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) f[e] = f[e] * inv * w[e];
         }
-        char* p = static_cast<char*>(second ? a.y[1] : a.y[0]) + row * a.row.D * ES;
-        row_store<IO, V>(p + at.a * ES, f);
-        row_store<IO, V>(p + at.b * ES, f + V);
+        turn<V, 1>(f, c, s);
+        out.template set<ADJACENT>(f);
+      } else {
+        // behind the sequence's end
+        if (cur.step == 0 && a.pairs) turns_fetch(a, &turns, cur.tok + pl.waves);
+        out.u[0] = out.u[1] = typename IoRow<IO, V>::words(0u);
+        if (!PACKED && v8_out && put) {
+          E4m3Row<V> v;
+          v.set(out, 0);
+          v.store(v8_out + row * D, off + pl.at.a, off + pl.at.b);
+          if (pl.j == 0) (s8_out + row)[pl.rg] = 0;
+        }
       }
+      if (put) out.store(y + row * D * ES, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
       load(i);
-      advance(a, &at_step, steps, waves);
+      advance(a, &cur, pl.steps, pl.waves);
     }
   }
 }
 
-// One operand a workgroup (blockIdx.y), so that its weights and the sums of
-// their gradients are one set of registers.
-template <int IO, int V, bool PACKED>
-__global__ __launch_bounds__(kQkThreads) void qk_backward_kernel(QkArgs a) {
-  __shared__ float trig_all[kQkWaves][2 * kMaxPairs];
+template <int IO, int V, bool PACKED, bool ADJACENT>
+__global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_kernel(QkArgs a) {
+  __shared__ __align__(16) float trig_all[kQkWaves][2 * kMaxPairs];
   __shared__ float sum[kRowMaxD];
   constexpr int ES = Io<IO>::bytes;
-  const bool second = blockIdx.y;
-  const int heads = second ? a.H[1] : a.H[0];
-  const RowView x = second ? a.x[1] : a.x[0], dx = second ? a.dx[1] : a.dx[0];
-  const uint8_t* v8 = second ? a.v8[1] : a.v8[0];
-  const uint8_t* s8 = second ? a.s8[1] : a.s8[0];
-  const char* dy = static_cast<const char*>(second ? a.y[1] : a.y[0]);
-  const float* wp = second ? a.w[1] : a.w[0];
-  const int lane = lane_id(), j = lane & (a.row.group - 1);
-  const int rg = lane / a.row.group, rpw = 64 / a.row.group;
-  const bool in_row = j < a.row.lanes;
-  const Slot at = row_slot<V>(j, a.pairs, a.adjacent);
-  const uint32_t tokens = (uint32_t)a.B * a.L, waves = gridDim.x * kQkWaves;
-  const int steps = (heads + rpw - 1) / rpw;
+  const Place<V, ADJACENT> pl(a);
+  const int D = a.row.D;
+  const uint32_t tokens = (uint32_t)a.B * a.L;
+  const RowView x = pl.second ? a.x[1] : a.x[0], dx = pl.second ? a.dx[1] : a.dx[0];
+  const uint8_t* v8 = pl.second ? a.v8[1] : a.v8[0];
+  const uint8_t* s8 = pl.second ? a.s8[1] : a.s8[0];
+  const char* dy = static_cast<const char*>(pl.second ? a.y[1] : a.y[0]);
   float* trig = trig_all[wave_id()];
-  float w[2 * V], dw[2 * V];
+  float w[2 * V], dw[2 * V], c[V], s[V];
+  pl.weights(a, w);
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) {
-    w[e] = wp && in_row ? wp[e < V ? at.a + e : at.b + e - V] : 1.f;
-    dw[e] = 0.f;
-  }
+  for (int e = 0; e < 2 * V; ++e) dw[e] = 0.f;
 
-  typename Source<IO, V, PACKED>::row xs[kQkBackAhead];
-  IoRow<IO, V> gs[kQkBackAhead];
-  int scale[kQkBackAhead];
-  Cursor ld, at_step;
+  typename Source<IO, V, PACKED>::row xs[kBackAhead];
+  IoRow<IO, V> gs[kBackAhead];
+  int scale[kBackAhead];
+  Cursor ld, cur;
   Turns turns;
-  set_token(a, &ld, blockIdx.x * kQkWaves + wave_id());
-  at_step = ld;
+  set_token(a, &ld, pl.first);
+  cur = ld;
+  trig_init(trig);
   if (a.pairs) {
     turns_init(a, &turns);
     turns_fetch(a, &turns, ld.tok);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) c[e] = 1.f, s[e] = 0.f;
   }
   auto load = [&](int i) {
-    const int h = ld.step * rpw + rg;
-    xs[i].clear();
-    gs[i].clear();
-    scale[i] = 0;
-    if (in_row && h < heads && ld.tok < tokens && ld.live) {
-      const int64_t row = (int64_t)ld.tok * heads + h;
-      gs[i].load(dy + row * a.row.D * ES, at);
+    if (ld.tok < tokens && ld.live) {
+      const uint32_t off = pl.row_of(ld.step) * D;
+      const int64_t row = (int64_t)ld.tok * pl.heads + ld.step * pl.rpw;
+      gs[i].load(dy + row * D * ES, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
       if (a.norm) {
         if constexpr (PACKED) {
-          xs[i].load(v8 + row * a.row.D, at);
-          scale[i] = s8[row];
+          xs[i].load(v8 + row * D, off + pl.at.a, off + pl.at.b);
+          scale[i] = (s8 + row)[pl.row_of(ld.step)];
         } else {
-          xs[i].load(static_cast<const char*>(x.p) +
-                         ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl) * ES + h * a.row.D * ES,
-                     at);
+          const char* p = static_cast<const char*>(x.p) +
+                          ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl + ld.step * pl.rpw * D) * ES;
+          xs[i].load(p, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
         }
       }
     }
-    advance(a, &ld, steps, waves);
+    advance(a, &ld, pl.steps, pl.waves);
   };
 #pragma unroll
-  for (int i = 0; i < kQkBackAhead; ++i) load(i);
+  for (int i = 0; i < kBackAhead; ++i) load(i);
 
-  float c[V], s[V];
-  while (at_step.tok < tokens) {
+  while (cur.tok < tokens) {
 #pragma unroll
-    for (int i = 0; i < kQkBackAhead; ++i) {
-      if (at_step.tok >= tokens) break;
-      if (at_step.step == 0 && a.pairs) {
-        token_turns<V>(a, turns, trig, j, c, s);
-        turns_fetch(a, &turns, at_step.tok + waves);
+    for (int i = 0; i < kBackAhead; ++i) {
+      if (cur.tok >= tokens) break;
+      const bool put = pl.writes(cur.step);
+      IoRow<IO, V> out;
+      if (cur.live) {
+        if (cur.step == 0 && a.pairs) {
+          token_turns<V>(a, turns, trig, pl.j, c, s);
+          turns_fetch(a, &turns, cur.tok + pl.waves);
+        }
+        float g[2 * V];
+        gs[i].template get<ADJACENT>(g);
+        turn<V, -1>(g, c, s);
+        if (a.norm) {
+          float f[2 * V], ss = 0.f, dot = 0.f;
+          if constexpr (PACKED) xs[i].template get<ADJACENT>(f, scale[i]);
+          else xs[i].template get<ADJACENT>(f);
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
+          ss = group_sum(pl.in_row ? ss : 0.f, a.row.group);
+          const float inv = row_inverse(fmaf(ss, a.c, a.eps));
+          // lanes without a row of their own add nothing to dw
+          const float own = put ? inv : 0.f;
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) {
+            dw[e] = fmaf(g[e] * own, f[e], dw[e]);
+            g[e] *= inv * w[e];
+            dot = fmaf(f[e], g[e], dot);
+          }
+          // dx = r g w - x (r^2 c) sum(x r g w)
+          dot = group_sum(pl.in_row ? dot : 0.f, a.row.group) * a.c * inv * inv;
+#pragma unroll
+          for (int e = 0; e < 2 * V; ++e) g[e] = fmaf(-f[e], dot, g[e]);
+        }
+        out.template set<ADJACENT>(g);
+      } else {
+        if (cur.step == 0 && a.pairs) turns_fetch(a, &turns, cur.tok + pl.waves);
+        out.u[0] = out.u[1] = typename IoRow<IO, V>::words(0u);
       }
-      const int h = at_step.step * rpw + rg;
-      float g[2 * V];
-      gs[i].get(g);
-      if (a.pairs) turn<V, -1>(g, c, s, a.adjacent);
-      if (a.norm) {
-        float f[2 * V], ss = 0.f, dot = 0.f;
-        xs[i].get(f);
-        if constexpr (PACKED) {
-          const float m = unpack_factor(scale[i]);
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) f[e] *= m;
-        }
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
-        const float inv = row_inverse(fmaf(group_sum(ss, a.row.group), a.c, a.eps));
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) {
-          f[e] *= inv;                     // x r
-          dw[e] = fmaf(g[e], f[e], dw[e]);
-          g[e] *= w[e];
-          dot = fmaf(f[e], g[e], dot);
-        }
-        dot = group_sum(dot, a.row.group) * a.c;
-#pragma unroll
-        for (int e = 0; e < 2 * V; ++e) g[e] = (g[e] - f[e] * dot) * inv;
-      }
-      if (in_row && h < heads) {
-        if (!at_step.live) {
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) g[e] = 0.f;
-        }
+      if (put) {
         char* p = const_cast<char*>(static_cast<const char*>(dx.p)) +
-                  ((int64_t)at_step.b * dx.sb + (int64_t)at_step.l * dx.sl) * ES +
-                  h * a.row.D * ES;
-        row_store<IO, V>(p + at.a * ES, g);
-        row_store<IO, V>(p + at.b * ES, g + V);
+                  ((int64_t)cur.b * dx.sb + (int64_t)cur.l * dx.sl + cur.step * pl.rpw * D) * ES;
+        const uint32_t off = pl.rg * D;
+        out.store(p, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
       }
       load(i);
-      advance(a, &at_step, steps, waves);
+      advance(a, &cur, pl.steps, pl.waves);
     }
   }
   if (!a.part) return;
@@ -368,84 +386,127 @@ __global__ __launch_bounds__(kQkThreads) void qk_backward_kernel(QkArgs a) {
   for (int e = 0; e < 2 * V; ++e)
     for (int o = a.row.group; o < 64; o <<= 1) dw[e] += __shfl_xor(dw[e], o);
   for (int k = 0; k < kQkWaves; ++k) {
-    if (wave_id() == k && lane < a.row.lanes) {
+    if (wave_id() == k && lane_id() < a.row.lanes) {
 #pragma unroll
-      for (int e = 0; e < 2 * V; ++e) {
-        const int d = e < V ? at.a + e : at.b + e - V;
-        sum[d] = k ? sum[d] + dw[e] : dw[e];
+      for (int m = 0; m < 2 * V; ++m) {
+        const int d = m < V ? pl.at.a + m : pl.at.b + m - V;
+        const float v = dw[pair_place<V, ADJACENT>(m)];
+        sum[d] = k ? sum[d] + v : v;
       }
     }
     __syncthreads();
   }
-  for (int d = threadIdx.x; d < a.row.D; d += kQkThreads)
-    a.part[((int64_t)blockIdx.x * 2 + second) * a.row.D + d] = sum[d];
+  for (int d = threadIdx.x; d < D; d += kQkThreads)
+    a.part[(int64_t)blockIdx.x * D + d] = sum[d];
 }
 
-// Sum of the workgroups' parts, in a fixed order: 32 columns a workgroup, 32
-// threads a column, each every 32nd row, then a tree.
+// Sum of the workgroups' parts, in a fixed order: 32 columns of an operand
+// (blockIdx.y) a workgroup, 32 threads a column, each every 32nd row, then a
+// tree.
 __global__ __launch_bounds__(1024) void qk_weights_kernel(QkArgs a, int wgs) {
   __shared__ float sum[32][33];
+  const int D = a.row.D, first = blockIdx.y ? a.split : 0, end = blockIdx.y ? wgs : a.split;
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   float v = 0.f;
-  if (col < 2 * a.row.D)
-    for (int r = slice; r < wgs; r += 32) v += a.part[(int64_t)r * 2 * a.row.D + col];
+  if (col < D) {
+#pragma unroll 8
+    for (int r = first + slice; r < end; r += 32) v += a.part[(int64_t)r * D + col];
+  }
   sum[slice][threadIdx.x & 31] = v;
   __syncthreads();
   for (int o = 16; o; o >>= 1) {
     if (slice < o) sum[slice][threadIdx.x & 31] += sum[slice + o][threadIdx.x & 31];
     __syncthreads();
   }
-  if (slice == 0 && col < 2 * a.row.D) {
-    const int which = col >= a.row.D;
-    (which ? a.dw[1] : a.dw[0])[col - which * a.row.D] = sum[0][threadIdx.x & 31];
+  if (slice == 0 && col < D) (blockIdx.y ? a.dw[1] : a.dw[0])[col] = sum[0][threadIdx.x & 31];
+}
+
+// Workgroups on each operand: one wave a token where there are no more than
+// `most`, else shared out by the steps of a token's rows.
+struct Shares {
+  int first, all;
+};
+static Shares shares(const QkArgs& a, int most) {
+  const int64_t need = ((int64_t)a.B * a.L + kQkWaves - 1) / kQkWaves;
+  if (2 * need <= most) return Shares{(int)need, (int)(2 * need)};
+  const int rpw = 64 / a.row.group;
+  const int64_t s0 = (a.H[0] + rpw - 1) / rpw, s1 = (a.H[1] + rpw - 1) / rpw;
+  int64_t n = (most * s0 + (s0 + s1) / 2) / (s0 + s1);
+  n = n < 1 ? 1 : n > most - 1 ? most - 1 : n;
+  const int64_t k = most - n < need ? most - n : need;
+  n = n < need ? n : need;
+  return Shares{(int)n, (int)(n + k)};
+}
+
+int64_t qk_backward_parts(int64_t tokens) {
+  const int64_t need = (tokens + kQkWaves - 1) / kQkWaves;
+  return 2 * need < kQkBackWgs ? 2 * need : kQkBackWgs;
+}
+
+template <bool PACKED, bool ADJACENT>
+static void forward_as(const QkArgs& a, int io, int wgs, hipStream_t s) {
+  const dim3 g(wgs), t(kQkThreads);
+  if (io == IO_BF16) {
+    if (a.row.V == 8)
+      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 8, PACKED, ADJACENT>), g, t, 0, s, a);
+    else if (a.row.V == 4)
+      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 4, PACKED, ADJACENT>), g, t, 0, s, a);
+    else
+      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 2, PACKED, ADJACENT>), g, t, 0, s, a);
+  } else {
+    if (a.row.V == 4)
+      hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 4, PACKED, ADJACENT>), g, t, 0, s, a);
+    else
+      hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 2, PACKED, ADJACENT>), g, t, 0, s, a);
   }
 }
 
-int qk_backward_wgs(int64_t tokens) {
-  const int64_t n = (tokens + kQkWaves - 1) / kQkWaves;
-  return (int)(n < kQkBackWgs ? n : kQkBackWgs);
-}
-
-template <bool PACKED>
-static hipError_t forward_as(const QkArgs& a, int io, hipStream_t s) {
-  const int64_t tokens = (int64_t)a.B * a.L, wgs = (tokens + kQkWaves - 1) / kQkWaves;
-  const dim3 g((unsigned)(wgs < kQkWgs ? wgs : kQkWgs)), t(kQkThreads);
-  if (io == IO_BF16) {
-    if (a.row.V == 8) hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 8, PACKED>), g, t, 0, s, a);
-    else if (a.row.V == 4)
-      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 4, PACKED>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 2, PACKED>), g, t, 0, s, a);
+hipError_t launch_qk_forward(const QkArgs& args, int io, bool packed, hipStream_t s) {
+  QkArgs a = args;
+  const Shares sh = shares(a, kQkWgs);
+  a.split = sh.first;
+  if (packed) {
+    if (a.adjacent) forward_as<true, true>(a, io, sh.all, s);
+    else forward_as<true, false>(a, io, sh.all, s);
   } else {
-    if (a.row.V == 4) hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 4, PACKED>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 2, PACKED>), g, t, 0, s, a);
+    if (a.adjacent) forward_as<false, true>(a, io, sh.all, s);
+    else forward_as<false, false>(a, io, sh.all, s);
   }
   return hipGetLastError();
 }
 
-hipError_t launch_qk_forward(const QkArgs& a, int io, bool packed, hipStream_t s) {
-  return packed ? forward_as<true>(a, io, s) : forward_as<false>(a, io, s);
-}
-
-template <bool PACKED>
-static hipError_t backward_as(const QkArgs& a, int io, hipStream_t s) {
-  const dim3 g(qk_backward_wgs((int64_t)a.B * a.L), 2), t(kQkThreads);
+template <bool PACKED, bool ADJACENT>
+static void backward_as(const QkArgs& a, int io, int wgs, hipStream_t s) {
+  const dim3 g(wgs), t(kQkThreads);
   if (io == IO_BF16) {
-    if (a.row.V == 8) hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 8, PACKED>), g, t, 0, s, a);
+    if (a.row.V == 8)
+      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 8, PACKED, ADJACENT>), g, t, 0, s, a);
     else if (a.row.V == 4)
-      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 4, PACKED>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 2, PACKED>), g, t, 0, s, a);
+      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 4, PACKED, ADJACENT>), g, t, 0, s, a);
+    else
+      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 2, PACKED, ADJACENT>), g, t, 0, s, a);
   } else {
-    if (a.row.V == 4) hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 4, PACKED>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 2, PACKED>), g, t, 0, s, a);
+    if (a.row.V == 4)
+      hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 4, PACKED, ADJACENT>), g, t, 0, s, a);
+    else
+      hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 2, PACKED, ADJACENT>), g, t, 0, s, a);
   }
-  return hipGetLastError();
 }
 
-hipError_t launch_qk_backward(const QkArgs& a, int io, bool packed, hipStream_t s) {
-  hipError_t e = packed ? backward_as<true>(a, io, s) : backward_as<false>(a, io, s);
+hipError_t launch_qk_backward(const QkArgs& args, int io, bool packed, hipStream_t s) {
+  QkArgs a = args;
+  const Shares sh = shares(a, kQkBackWgs);
+  a.split = sh.first;
+  if (packed) {
+    if (a.adjacent) backward_as<true, true>(a, io, sh.all, s);
+    else backward_as<true, false>(a, io, sh.all, s);
+  } else {
+    if (a.adjacent) backward_as<false, true>(a, io, sh.all, s);
+    else backward_as<false, false>(a, io, sh.all, s);
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  hipLaunchKernelGGL(qk_weights_kernel, dim3((2 * a.row.D + 31) / 32), dim3(1024), 0, s, a,
-                     qk_backward_wgs((int64_t)a.B * a.L));
+  hipLaunchKernelGGL(qk_weights_kernel, dim3((a.row.D + 31) / 32, 2), dim3(1024), 0, s, a, sh.all);
   return hipGetLastError();
 }
 
