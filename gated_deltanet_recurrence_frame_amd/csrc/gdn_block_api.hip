@@ -103,7 +103,7 @@ struct RowUse {
   int es;
 };
 bool fits(int V, int B, int L, int D, int pairs, const RowUse* use, int n) {
-  if (D % (2 * V) || pairs % V) return false;
+  if (D % V || D / V > 64 || pairs % V) return false;
   for (int i = 0; i < n; ++i) {
     if (!use[i].p) continue;
     if (!aligned(use[i].p, V * use[i].es)) return false;
@@ -119,7 +119,7 @@ RowShape row_shape(int B, int L, int D, int pairs, int io, const RowUse* use, in
   for (int V = io == IO_BF16 ? 8 : 4; V >= 2 && !r.V; V /= 2)
     if (fits(V, B, L, D, pairs, use, n)) r.V = V;
   if (!r.V) return r;
-  r.lanes = D / (2 * r.V);
+  r.lanes = D / r.V;
   for (r.group = 1; r.group < r.lanes;) r.group *= 2;
   return r;
 }

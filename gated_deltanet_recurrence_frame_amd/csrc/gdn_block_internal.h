@@ -19,10 +19,9 @@ struct RowView {
   int64_t sb, sl;
 };
 
-// How a row of D values lies over lanes: every lane holds two pieces of V
-// elements, so that both members of a rotated pair are in one lane.  `lanes`
-// lanes hold a row, `group` (the power of two from there) are given to it;
-// a wave holds 64 / group rows.
+// How a row of D values lies over lanes: a piece of V elements each, `lanes`
+// of them, of the `group` (the power of two from there, at most 64) that is
+// given to a row; a wave holds 64 / group rows.
 struct RowShape {
   int D, lanes, group;
   int V;

@@ -29,21 +29,25 @@ __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const bool in_row = j < a.row.lanes;
   const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
-  const uint32_t at = in_row ? 2 * j * V : 0;   // a lane without a piece reads the row's first
+  const uint32_t at = in_row ? j * V : 0;   // a lane without a piece reads the row's first
   IoRow<IO, V> x[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
-    x[i].load(io_row<IO>(a, r < rows ? r : rows - 1), at * ES, (at + V) * ES);
+    x[i].load(io_row<IO>(a, r < rows ? r : rows - 1), at * ES);
   }
+  float top[kPackRows];
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) top[i] = row_max<IO, V>(x[i]);
+  group_max<kPackRows>(top, a.row.group);
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const uint32_t r = base + i * rpw;
-    const int s = scale_byte(group_max(row_max<IO, V>(x[i]), a.row.group));
+    const int s = scale_byte(top[i]);
     E4m3Row<V> v;
     v.set(x[i], s);
     if (r < rows) {
-      if (in_row) v.store(static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D, at, at + V);
+      if (in_row) v.store(static_cast<uint8_t*>(a.v) + (int64_t)r * a.row.D, at);
       if (j == 0) static_cast<uint8_t*>(a.scale)[r] = (uint8_t)s;
     }
   }
@@ -57,14 +61,14 @@ __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
   if (j >= a.row.lanes) return;
-  const uint32_t at = 2 * j * V;
+  const uint32_t at = j * V;
   E4m3Row<V> v[kPackRows];
   int s[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     uint32_t r = base + i * rpw;
     r = r < rows ? r : rows - 1;
-    v[i].load(static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D, at, at + V);
+    v[i].load(static_cast<const uint8_t*>(a.v) + (int64_t)r * a.row.D, at);
     s[i] = static_cast<const uint8_t*>(a.scale)[r];
   }
 #pragma unroll
@@ -73,7 +77,7 @@ __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
     if (r < rows) {
       IoRow<IO, V> x;
       v[i].get(&x, s[i]);
-      x.store(const_cast<char*>(io_row<IO>(a, r)), at * ES, (at + V) * ES);
+      x.store(const_cast<char*>(io_row<IO>(a, r)), at * ES);
     }
   }
 }

@@ -5,25 +5,31 @@
 // sums are then one set of registers); the workgroups are shared out by the
 // operands' rows.  A wave takes one token after the other: the rows of its
 // heads lie next to each other over groups of lanes (RowShape), 64 / group
-// heads a step, and are loaded kAhead steps before they are used.  The
+// heads at once, kRows times that a step (the reductions over a row's lanes
+// are chains; two rows a lane go through them side by side), and are loaded
+// kAhead steps before they are used.  The
 // rotation's cosines and sines are the same for every head of a token, so the
 // wave's lanes form one pair's each, once a token (the angle in turns in 64
 // bits, reduced to [-1/2, 1/2] before it is rounded; the hardware's sine and
 // cosine of turns are then within 2.1 2^-24, measured over that range), and
-// pass them through LDS; the two members of a pair are in one lane
-// (row_slot), so the rotation itself moves nothing between lanes.
+// pass them through LDS.  A lane has one piece of a row, so that a step's
+// accesses are whole rows; the partners of its elements are in the piece
+// itself (adjacent pairs) or in another lane's (halves), which it gets as
+// loaded, through the LDS crossbar.
 #include "gdn_rows.h"
 
 namespace gdn {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkWaves = kQkThreads / 64;
-constexpr int kAhead = 4;           // steps loaded ahead (forward)
-constexpr int kBackAhead = 3;       // (backward)
+constexpr int kRows = 2;            // rows of a lane in a step (forward)
+constexpr int kBackRows = 2;        // (backward)
+constexpr int kAhead = 2;           // steps loaded ahead (forward)
+constexpr int kBackAhead = 1;       // (backward)
 // Workgroups at most: as many as the card holds at once (256 CUs, 4 SIMDs
 // with one wave of a workgroup each) at the waves a SIMD that the registers
 // are bounded for; one more would run alone at the end.
-constexpr int kWavesPerSimd = 4, kBackWavesPerSimd = 3;
+constexpr int kWavesPerSimd = 4, kBackWavesPerSimd = 4;
 constexpr int kQkWgs = 256 * kWavesPerSimd;
 constexpr int kQkBackWgs = 256 * kBackWavesPerSimd;
 constexpr int kMaxPairs = kRowMaxD / 2;
@@ -77,16 +83,8 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// trig[2 m], trig[2 m + 1]: cosine and sine of pair m; (1, 0) behind the last
-// pair, for the elements that are not turned.
-__device__ __forceinline__ void trig_init(float* trig) {
-#pragma unroll
-  for (int i = 0; i < 2 * kMaxPairs / 64; ++i)
-    trig[lane_id() + 64 * i] = (lane_id() & 1) ? 0.f : 1.f;
-}
-template <int V>
-__device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, float* trig, int j,
-                                            float* c, float* s) {
+// trig[2 m], trig[2 m + 1]: cosine and sine of pair m.
+__device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, float* trig) {
   wave_lds_sync();   // the last token's reads are done
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -99,25 +97,6 @@ __device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, flo
     }
   }
   wave_lds_sync();
-#pragma unroll
-  for (int e = 0; e < V; e += 2) {
-    const f32x4 q = *reinterpret_cast<const f32x4*>(trig + 2 * (j * V + e));
-    c[e] = q[0];
-    s[e] = q[1];
-    c[e + 1] = q[2];
-    s[e + 1] = q[3];
-  }
-}
-
-// Turn a lane's V pairs by phi (SIGN 1) or -phi (SIGN -1).
-template <int V, int SIGN>
-__device__ __forceinline__ void turn(float* f, const float* c, const float* s) {
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const float x = f[e], y = f[e + V], sn = SIGN * s[e];
-    f[e] = x * c[e] - y * sn;
-    f[e + V] = x * sn + y * c[e];
-  }
 }
 
 // 1 / sqrt of a row's argument (to 1.6 2^-24, measured); 0 where that is 0,
@@ -127,14 +106,17 @@ __device__ __forceinline__ float row_inverse(float ss) {
 }
 
 // What a workgroup is on: an operand, and how its lanes lie over the rows.
-template <int V, bool ADJACENT>
+template <int IO, int V, bool ADJACENT, int ROWS>
 struct Place {
   bool second;
   int heads, steps;
   uint32_t first, waves;   // the wave's first token, the operand's waves
   int j, rg, rpw;
   bool in_row;
-  Slot at;
+  int at;                  // the lane's first element; a lane without a piece reads the row's first
+  bool turned;             // its elements are rotated
+  int pair;                // the first one's pair
+  int partner;             // the lane with the partners, times 4
 
   __device__ __forceinline__ explicit Place(const QkArgs& a) {
     second = (int)blockIdx.x >= a.split;
@@ -146,26 +128,72 @@ struct Place {
     j = lane_id() & (a.row.group - 1);
     rg = lane_id() / a.row.group;
     rpw = 64 / a.row.group;
-    steps = (heads + rpw - 1) / rpw;
+    steps = (heads + ROWS * rpw - 1) / (ROWS * rpw);
     in_row = j < a.row.lanes;
-    at = row_slot<V, ADJACENT>(in_row ? j : 0, a.pairs);   // others read the first piece
+    at = in_row ? j * V : 0;
+    turned = in_row && at < 2 * a.pairs;
+    const bool later = !ADJACENT && at >= a.pairs;
+    pair = !turned ? 0 : ADJACENT ? at / 2 : later ? at - a.pairs : at;
+    partner = 4 * (lane_id() + (turned && !ADJACENT ? (later ? -1 : 1) * (a.pairs / V) : 0));
   }
-  // the lane's row in a step, or the step's last (read, not written)
-  __device__ __forceinline__ uint32_t row_of(int step) const {
-    const int left = heads - step * rpw - 1;
-    return rg < left ? rg : left;
+  // the first head of a step's u-th row
+  __device__ __forceinline__ int head(int step, int u) const { return (step * ROWS + u) * rpw; }
+  // Rows of a step that there are at all (the same for all lanes).
+  __device__ __forceinline__ bool both(int step) const {
+    return ROWS == 2 && head(step, 1) < heads;
   }
-  __device__ __forceinline__ bool writes(int step) const {
-    return in_row && rg < heads - step * rpw;
+  // the lane's head, or the last (read, not written)
+  __device__ __forceinline__ uint32_t head_of(int step, int u) const {
+    const int h = head(step, u) + rg;
+    return h < heads ? h : heads - 1;
   }
-  // the lane's weights (1 without), in the order of its floats
-  __device__ __forceinline__ void weights(const QkArgs& a, float* w) const {
+  __device__ __forceinline__ bool writes(int step, int u) const {
+    return in_row && head(step, u) + rg < heads;
+  }
+  // element e's weight and its partner's (1 without)
+  __device__ __forceinline__ void weights(const QkArgs& a, float* w, float* wp) const {
     const float* p = second ? a.w[1] : a.w[0];
+    const int far = !turned || ADJACENT ? 0 : at >= a.pairs ? -a.pairs : a.pairs;
 #pragma unroll
-    for (int m = 0; m < 2 * V; ++m)
-      w[pair_place<V, ADJACENT>(m)] = p ? p[m < V ? at.a + m : at.b + m - V] : 1.f;
+    for (int e = 0; e < V; ++e) {
+      w[e] = p ? p[at + e] : 1.f;
+      wp[e] = p ? p[ADJACENT ? at + (e ^ 1) : at + e + far] : 1.f;
+    }
+  }
+  // A rotation of row x by phi (SIGN 1) or -phi (SIGN -1) is x_e c_e + x'_e
+  // s_e with x' the partners: first members subtract theirs, second ones add.
+  template <int SIGN>
+  __device__ __forceinline__ void coefficients(const QkArgs& a, const float* trig, float* c,
+                                               float* s) const {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const bool later = ADJACENT ? e & 1 : at >= a.pairs;
+      const f32x2 t = *reinterpret_cast<const f32x2*>(trig + 2 * (pair + (ADJACENT ? e / 2 : e)));
+      c[e] = turned ? t[0] : 1.f;
+      s[e] = (SIGN > 0) == later ? t[1] : -t[1];
+    }
+  }
+  // the partners of the lane's elements; 0 where it has none
+  __device__ __forceinline__ IoRow<IO, V> partners(const IoRow<IO, V>& x) const {
+    IoRow<IO, V> p;
+    if constexpr (ADJACENT) {
+#pragma unroll
+      for (int e = 0; e < IoRow<IO, V>::kWords; ++e) {
+        if constexpr (IO == IO_BF16) p.u[e] = __builtin_amdgcn_alignbit(x.u[e], x.u[e], 16);
+        else p.u[e] = x.u[e ^ 1];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < IoRow<IO, V>::kWords; ++e)
+        p.u[e] = __builtin_amdgcn_ds_bpermute(partner, x.u[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < IoRow<IO, V>::kWords; ++e) p.u[e] = turned ? p.u[e] : 0u;
+    return p;
   }
 };
+
+template <int N> struct Count { static constexpr int value = N; };
 
 template <int IO, int V, bool PACKED> struct Source { typedef IoRow<IO, V> row; };
 template <int IO, int V> struct Source<IO, V, true> { typedef E4m3Row<V> row; };
@@ -174,7 +202,7 @@ template <int IO, int V, bool PACKED, bool ADJACENT>
 __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(QkArgs a) {
   __shared__ __align__(16) float trig_all[kQkWaves][2 * kMaxPairs];
   constexpr int ES = Io<IO>::bytes;
-  const Place<V, ADJACENT> pl(a);
+  const Place<IO, V, ADJACENT, kRows> pl(a);
   const int D = a.row.D;
   const uint32_t tokens = (uint32_t)a.B * a.L;
   const RowView x = pl.second ? a.x[1] : a.x[0];
@@ -184,34 +212,36 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
   uint8_t* s8_out = pl.second ? a.s8_out[1] : a.s8_out[0];
   char* y = static_cast<char*>(pl.second ? a.y[1] : a.y[0]);
   float* trig = trig_all[wave_id()];
-  float w[2 * V], c[V], s[V];
-  pl.weights(a, w);
+  // y_e = r (x_e c_e + x'_e s_e), the weights within c and s
+  float w[V], wp[V], c[V], s[V];
+  pl.weights(a, w, wp);
+#pragma unroll
+  for (int e = 0; e < V; ++e) c[e] = w[e], s[e] = 0.f;
 
-  typename Source<IO, V, PACKED>::row ahead[kAhead];
-  int scale[kAhead];
+  typename Source<IO, V, PACKED>::row ahead[kAhead][kRows];
+  int scale[kAhead][kRows];
   Cursor ld, cur;
   Turns turns;
   set_token(a, &ld, pl.first);
   cur = ld;
-  trig_init(trig);
   if (a.pairs) {
     turns_init(a, &turns);
     turns_fetch(a, &turns, ld.tok);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) c[e] = 1.f, s[e] = 0.f;
   }
   auto load = [&](int i) {
     if (ld.tok < tokens && ld.live) {
-      const uint32_t off = pl.row_of(ld.step) * D;
-      if constexpr (PACKED) {
-        const int64_t row = (int64_t)ld.tok * pl.heads + ld.step * pl.rpw;
-        ahead[i].load(v8 + row * D, off + pl.at.a, off + pl.at.b);
-        scale[i] = (s8 + row)[pl.row_of(ld.step)];
-      } else {
-        const char* p = static_cast<const char*>(x.p) +
-                        ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl + ld.step * pl.rpw * D) * ES;
-        ahead[i].load(p, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const uint32_t h = pl.head_of(ld.step, u);
+        if constexpr (PACKED) {
+          const int64_t row = (int64_t)ld.tok * pl.heads;
+          ahead[i][u].load(v8 + row * D, h * D + pl.at);
+          scale[i][u] = (s8 + row)[h];
+        } else {
+          ahead[i][u].load(static_cast<const char*>(x.p) +
+                               ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl) * ES,
+                           (h * D + pl.at) * ES);
+        }
       }
     }
     advance(a, &ld, pl.steps, pl.waves);
@@ -219,56 +249,99 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(i);
 
+  // N rows of the lane's, of step cur
+  auto process = [&](auto count, int i) {
+    constexpr int N = decltype(count)::value;
+    const int64_t row = (int64_t)cur.tok * pl.heads;
+    IoRow<IO, V> out[N];
+    if (cur.live) {
+      IoRow<IO, V> in[N];
+      float f[N][V], inv[N];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        if constexpr (PACKED) ahead[i][u].get(&in[u], scale[i][u]);
+        else in[u] = ahead[i][u];
+        in[u].get(f[u]);
+        inv[u] = 1.f;
+      }
+      if (!PACKED && v8_out) {
+        float top[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) top[u] = row_max<IO, V>(in[u]);
+        group_max<N>(top, a.row.group);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          const int sb = scale_byte(top[u]);
+          E4m3Row<V> v;
+          v.set(in[u], sb);
+          if (pl.writes(cur.step, u)) {
+            const uint32_t h = pl.head(cur.step, u) + pl.rg;
+            v.store(v8_out + row * D, h * D + pl.at);
+            if (pl.j == 0) (s8_out + row)[h] = (uint8_t)sb;
+          }
+        }
+      }
+      if (a.norm) {
+        float ss[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          ss[u] = 0.f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) ss[u] = fmaf(f[u][e], f[u][e], ss[u]);
+          ss[u] = pl.in_row ? ss[u] : 0.f;
+        }
+        group_sum<N>(ss, a.row.group);
+#pragma unroll
+        for (int u = 0; u < N; ++u) inv[u] = row_inverse(fmaf(ss[u], a.c, a.eps));
+      }
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        if (a.pairs) {
+          float g[V];
+          pl.partners(in[u]).get(g);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[u][e] = fmaf(g[e], s[e], f[u][e] * c[e]) * inv[u];
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[u][e] = f[u][e] * c[e] * inv[u];
+        }
+        out[u].set(f[u]);
+      }
+    } else {
+      // behind the sequence's end
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        out[u].u = typename IoRow<IO, V>::words(0u);
+        if (!PACKED && v8_out && pl.writes(cur.step, u)) {
+          const uint32_t h = pl.head(cur.step, u) + pl.rg;
+          E4m3Row<V> v;
+          v.set(out[u], 0);
+          v.store(v8_out + row * D, h * D + pl.at);
+          if (pl.j == 0) (s8_out + row)[h] = 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      if (pl.writes(cur.step, u))
+        out[u].store(y + row * D * ES, ((pl.head(cur.step, u) + pl.rg) * D + pl.at) * ES);
+  };
+
   while (cur.tok < tokens) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (cur.tok >= tokens) break;
-      const int64_t row = (int64_t)cur.tok * pl.heads + cur.step * pl.rpw;
-      const bool put = pl.writes(cur.step);
-      const uint32_t off = pl.rg * D;
-      IoRow<IO, V> out;
-      if (cur.live) {
-        if (cur.step == 0 && a.pairs) {
-          token_turns<V>(a, turns, trig, pl.j, c, s);
-          turns_fetch(a, &turns, cur.tok + pl.waves);
-        }
-        float f[2 * V], ss = 0.f;
-        if constexpr (PACKED) {
-          ahead[i].template get<ADJACENT>(f, scale[i]);
-        } else {
-          ahead[i].template get<ADJACENT>(f);
-          if (v8_out) {
-            const int sb = scale_byte(group_max(row_max<IO, V>(ahead[i]), a.row.group));
-            E4m3Row<V> v;
-            v.set(ahead[i], sb);
-            if (put) {
-              v.store(v8_out + row * D, off + pl.at.a, off + pl.at.b);
-              if (pl.j == 0) (s8_out + row)[pl.rg] = (uint8_t)sb;
-            }
-          }
-        }
-        if (a.norm) {
+      if (cur.step == 0 && a.pairs) {
+        if (cur.live) {
+          token_turns(a, turns, trig);
+          pl.template coefficients<1>(a, trig, c, s);
 #pragma unroll
-          for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
-          ss = group_sum(pl.in_row ? ss : 0.f, a.row.group);
-          const float inv = row_inverse(fmaf(ss, a.c, a.eps));
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) f[e] = f[e] * inv * w[e];
+          for (int e = 0; e < V; ++e) c[e] *= w[e], s[e] *= wp[e];
         }
-        turn<V, 1>(f, c, s);
-        out.template set<ADJACENT>(f);
-      } else {
-        // behind the sequence's end
-        if (cur.step == 0 && a.pairs) turns_fetch(a, &turns, cur.tok + pl.waves);
-        out.u[0] = out.u[1] = typename IoRow<IO, V>::words(0u);
-        if (!PACKED && v8_out && put) {
-          E4m3Row<V> v;
-          v.set(out, 0);
-          v.store(v8_out + row * D, off + pl.at.a, off + pl.at.b);
-          if (pl.j == 0) (s8_out + row)[pl.rg] = 0;
-        }
+        turns_fetch(a, &turns, cur.tok + pl.waves);
       }
-      if (put) out.store(y + row * D * ES, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
+      if (pl.both(cur.step)) process(Count<kRows>(), i);
+      else process(Count<1>(), i);
       load(i);
       advance(a, &cur, pl.steps, pl.waves);
     }
@@ -280,7 +353,7 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
   __shared__ __align__(16) float trig_all[kQkWaves][2 * kMaxPairs];
   __shared__ float sum[kRowMaxD];
   constexpr int ES = Io<IO>::bytes;
-  const Place<V, ADJACENT> pl(a);
+  const Place<IO, V, ADJACENT, kBackRows> pl(a);
   const int D = a.row.D;
   const uint32_t tokens = (uint32_t)a.B * a.L;
   const RowView x = pl.second ? a.x[1] : a.x[0], dx = pl.second ? a.dx[1] : a.dx[0];
@@ -288,39 +361,38 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
   const uint8_t* s8 = pl.second ? a.s8[1] : a.s8[0];
   const char* dy = static_cast<const char*>(pl.second ? a.y[1] : a.y[0]);
   float* trig = trig_all[wave_id()];
-  float w[2 * V], dw[2 * V], c[V], s[V];
-  pl.weights(a, w);
+  float w[V], wp[V], dw[V], c[V], s[V];
+  pl.weights(a, w, wp);
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) dw[e] = 0.f;
+  for (int e = 0; e < V; ++e) dw[e] = 0.f, c[e] = 1.f, s[e] = 0.f;
 
-  typename Source<IO, V, PACKED>::row xs[kBackAhead];
-  IoRow<IO, V> gs[kBackAhead];
-  int scale[kBackAhead];
+  typename Source<IO, V, PACKED>::row xs[kBackAhead][kBackRows];
+  IoRow<IO, V> gs[kBackAhead][kBackRows];
+  int scale[kBackAhead][kBackRows];
   Cursor ld, cur;
   Turns turns;
   set_token(a, &ld, pl.first);
   cur = ld;
-  trig_init(trig);
   if (a.pairs) {
     turns_init(a, &turns);
     turns_fetch(a, &turns, ld.tok);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) c[e] = 1.f, s[e] = 0.f;
   }
   auto load = [&](int i) {
     if (ld.tok < tokens && ld.live) {
-      const uint32_t off = pl.row_of(ld.step) * D;
-      const int64_t row = (int64_t)ld.tok * pl.heads + ld.step * pl.rpw;
-      gs[i].load(dy + row * D * ES, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
-      if (a.norm) {
-        if constexpr (PACKED) {
-          xs[i].load(v8 + row * D, off + pl.at.a, off + pl.at.b);
-          scale[i] = (s8 + row)[pl.row_of(ld.step)];
-        } else {
-          const char* p = static_cast<const char*>(x.p) +
-                          ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl + ld.step * pl.rpw * D) * ES;
-          xs[i].load(p, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
+#pragma unroll
+      for (int u = 0; u < kBackRows; ++u) {
+        const uint32_t h = pl.head_of(ld.step, u);
+        const int64_t row = (int64_t)ld.tok * pl.heads;
+        gs[i][u].load(dy + row * D * ES, (h * D + pl.at) * ES);
+        if (a.norm) {
+          if constexpr (PACKED) {
+            xs[i][u].load(v8 + row * D, h * D + pl.at);
+            scale[i][u] = (s8 + row)[h];
+          } else {
+            xs[i][u].load(static_cast<const char*>(x.p) +
+                              ((int64_t)ld.b * x.sb + (int64_t)ld.l * x.sl) * ES,
+                          (h * D + pl.at) * ES);
+          }
         }
       }
     }
@@ -329,52 +401,83 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
 #pragma unroll
   for (int i = 0; i < kBackAhead; ++i) load(i);
 
+  auto process = [&](auto count, int i) {
+    constexpr int N = decltype(count)::value;
+    IoRow<IO, V> out[N];
+    if (cur.live) {
+      float g[N][V];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        gs[i][u].get(g[u]);
+        if (a.pairs) {
+          float h[V];
+          pl.partners(gs[i][u]).get(h);
+#pragma unroll
+          for (int e = 0; e < V; ++e) g[u][e] = fmaf(h[e], s[e], g[u][e] * c[e]);
+        }
+      }
+      if (a.norm) {
+        float f[N][V], ss[N], dot[N], inv[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          if constexpr (PACKED) xs[i][u].get(f[u], scale[i][u]);
+          else xs[i][u].get(f[u]);
+          ss[u] = 0.f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) ss[u] = fmaf(f[u][e], f[u][e], ss[u]);
+          ss[u] = pl.in_row ? ss[u] : 0.f;
+        }
+        group_sum<N>(ss, a.row.group);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          inv[u] = row_inverse(fmaf(ss[u], a.c, a.eps));
+          // lanes without a row of their own add nothing to dw, nor to the dot
+          const float own = pl.writes(cur.step, u) ? inv[u] : 0.f;
+          dot[u] = 0.f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            g[u][e] *= own;
+            dw[e] = fmaf(g[u][e], f[u][e], dw[e]);
+            g[u][e] *= w[e];
+            dot[u] = fmaf(f[u][e], g[u][e], dot[u]);
+          }
+        }
+        // dx = r g w - x (r^2 c) sum(x r g w)
+        group_sum<N>(dot, a.row.group);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          const float k = dot[u] * a.c * inv[u] * inv[u];
+#pragma unroll
+          for (int e = 0; e < V; ++e) g[u][e] = fmaf(-f[u][e], k, g[u][e]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < N; ++u) out[u].set(g[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) out[u].u = typename IoRow<IO, V>::words(0u);
+    }
+    char* p = const_cast<char*>(static_cast<const char*>(dx.p)) +
+              ((int64_t)cur.b * dx.sb + (int64_t)cur.l * dx.sl) * ES;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      if (pl.writes(cur.step, u))
+        out[u].store(p, ((pl.head(cur.step, u) + pl.rg) * D + pl.at) * ES);
+  };
+
   while (cur.tok < tokens) {
 #pragma unroll
     for (int i = 0; i < kBackAhead; ++i) {
       if (cur.tok >= tokens) break;
-      const bool put = pl.writes(cur.step);
-      IoRow<IO, V> out;
-      if (cur.live) {
-        if (cur.step == 0 && a.pairs) {
-          token_turns<V>(a, turns, trig, pl.j, c, s);
-          turns_fetch(a, &turns, cur.tok + pl.waves);
+      if (cur.step == 0 && a.pairs) {
+        if (cur.live) {
+          token_turns(a, turns, trig);
+          pl.template coefficients<-1>(a, trig, c, s);
         }
-        float g[2 * V];
-        gs[i].template get<ADJACENT>(g);
-        turn<V, -1>(g, c, s);
-        if (a.norm) {
-          float f[2 * V], ss = 0.f, dot = 0.f;
-          if constexpr (PACKED) xs[i].template get<ADJACENT>(f, scale[i]);
-          else xs[i].template get<ADJACENT>(f);
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
-          ss = group_sum(pl.in_row ? ss : 0.f, a.row.group);
-          const float inv = row_inverse(fmaf(ss, a.c, a.eps));
-          // lanes without a row of their own add nothing to dw
-          const float own = put ? inv : 0.f;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            dw[e] = fmaf(g[e] * own, f[e], dw[e]);
-            g[e] *= inv * w[e];
-            dot = fmaf(f[e], g[e], dot);
-          }
-          // dx = r g w - x (r^2 c) sum(x r g w)
-          dot = group_sum(pl.in_row ? dot : 0.f, a.row.group) * a.c * inv * inv;
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) g[e] = fmaf(-f[e], dot, g[e]);
-        }
-        out.template set<ADJACENT>(g);
-      } else {
-        if (cur.step == 0 && a.pairs) turns_fetch(a, &turns, cur.tok + pl.waves);
-        out.u[0] = out.u[1] = typename IoRow<IO, V>::words(0u);
+        turns_fetch(a, &turns, cur.tok + pl.waves);
       }
-      if (put) {
-        char* p = const_cast<char*>(static_cast<const char*>(dx.p)) +
-                  ((int64_t)cur.b * dx.sb + (int64_t)cur.l * dx.sl + cur.step * pl.rpw * D) * ES;
-        const uint32_t off = pl.rg * D;
-        out.store(p, (off + pl.at.a) * ES, (off + pl.at.b) * ES);
-      }
+      if (pl.both(cur.step)) process(Count<kBackRows>(), i);
+      else process(Count<1>(), i);
       load(i);
       advance(a, &cur, pl.steps, pl.waves);
     }
@@ -383,16 +486,12 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
   // the workgroup's sum, in a fixed order: the row groups of each wave, then
   // the waves in turn
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e)
+  for (int e = 0; e < V; ++e)
     for (int o = a.row.group; o < 64; o <<= 1) dw[e] += __shfl_xor(dw[e], o);
   for (int k = 0; k < kQkWaves; ++k) {
     if (wave_id() == k && lane_id() < a.row.lanes) {
 #pragma unroll
-      for (int m = 0; m < 2 * V; ++m) {
-        const int d = m < V ? pl.at.a + m : pl.at.b + m - V;
-        const float v = dw[pair_place<V, ADJACENT>(m)];
-        sum[d] = k ? sum[d] + v : v;
-      }
+      for (int e = 0; e < V; ++e) sum[pl.at + e] = k ? sum[pl.at + e] + dw[e] : dw[e];
     }
     __syncthreads();
   }
@@ -430,7 +529,7 @@ static Shares shares(const QkArgs& a, int most) {
   const int64_t need = ((int64_t)a.B * a.L + kQkWaves - 1) / kQkWaves;
   if (2 * need <= most) return Shares{(int)need, (int)(2 * need)};
   const int rpw = 64 / a.row.group;
-  const int64_t s0 = (a.H[0] + rpw - 1) / rpw, s1 = (a.H[1] + rpw - 1) / rpw;
+  const int64_t s0 = (a.H[0] + rpw - 1) / rpw, s1 = (a.H[1] + rpw - 1) / rpw;   // rows
   int64_t n = (most * s0 + (s0 + s1) / 2) / (s0 + s1);
   n = n < 1 ? 1 : n > most - 1 ? most - 1 : n;
   const int64_t k = most - n < need ? most - n : need;

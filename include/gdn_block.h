@@ -24,7 +24,9 @@
  *   - io pointers need the alignment of two elements for qk and pack8 (4
  *     bytes for bf16, 8 for fp32) and of one element for lrec, fp32 and
  *     int32 pointers 4 bytes, workspaces and saved buffers 16; strides of qk
- *     and pack8 are even.  Rows that are 16-byte aligned are the fast case.
+ *     and pack8 are even.  Heads D > 128 need four elements' alignment in
+ *     place of two (pointers, strides and a rotation's number of pairs), else
+ *     GDN_ERR_MISALIGNED.  Rows that are 16-byte aligned are the fast case.
  *   - Sizes are at least 1; B * L at most 2^31 - 1, at most 2^40 elements a
  *     tensor, strides at most 2^40.
  *   - `lengths` is NULL or B device int32s, the number of tokens of each

@@ -168,6 +168,15 @@ def test_qk_pointers(lib):
     assert qk_forward(lib, qk_problem(q_stride=(1280, 257))) == "GDN_ERR_MISALIGNED"
 
 
+def test_wide_heads_need_four_elements(lib):
+    # 64 lanes hold a row in pieces of 2 elements up to D = 128
+    for D, pairs, ok in ((256, 128, True), (256, 126, False), (128, 62, True), (200, 50, False)):
+        p = block.make_qk_problem(1, 2, 1, 1, D, "bf16", "rms", 1e-6, (pairs,))
+        got = qk_forward(lib, p, qo=at(0) if ok else at(5))
+        assert got == ("GDN_ERR_ALIASING" if ok else "GDN_ERR_MISALIGNED"), (D, pairs)
+    assert pack(lib, {"D": 256, "H": 1, "stride": (768, 258)}) == "GDN_ERR_MISALIGNED"
+
+
 def test_qk_aliasing(lib):
     p = qk_problem()
     assert qk_forward(lib, p, qo=at(0)) == "GDN_ERR_ALIASING"              # in place
