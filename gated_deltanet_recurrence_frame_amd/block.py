@@ -97,46 +97,58 @@ def _device(device):
     return device
 
 
-def _call(dev, name, *args):
-    """The entry point on `dev`'s current stream, with `dev` current."""
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() != dev.index:
+def _call(dev, f, name, *args):
+    """The entry point f on `dev`'s current stream, with `dev` current."""
+    i = dev.index
+    if torch.cuda.current_device() != i:
         with torch.cuda.device(dev):
-            _check(f(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+            _check(f(*args, torch._C._cuda_getCurrentRawStream(i)), name)
     else:
-        _check(f(*args, torch.cuda.current_stream(dev).cuda_stream), name)
+        code = f(*args, torch._C._cuda_getCurrentRawStream(i))
+        if code:
+            _check(code, name)
 
 
-def _view(t, name, dtype, shape, dev):
+def _inner(shape):
+    """Strides of the dimensions behind the tokens when they are contiguous."""
+    return (shape[3], 1) if len(shape) == 4 else (1,)
+
+
+def _view(t, name, dtype, shape, dev, inner=None):
     """Check a [B, L, ...] tensor whose dimensions behind the tokens are
-    contiguous; returns its strides of batches and tokens (0 where there is
-    one of them)."""
-    if t is None:
-        raise ValueError("%s is required" % name)
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
+    contiguous; returns its strides of batches and tokens (those of a single
+    one count for nothing)."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != dev:
         _need(t, name, dtype, shape, dev)
-    st, inner = t.stride(), 1
-    for i in range(len(shape) - 1, 1, -1):
-        if shape[i] != 1 and st[i] != inner:
-            raise ValueError("%s must be contiguous behind its tokens" % name)
-        inner *= shape[i]
-    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+    st = t.stride()
+    inner = inner or _inner(shape)
+    if st[2:] != inner:
+        for n, a, b in zip(shape[2:], st[2:], inner):
+            if n != 1 and a != b:
+                raise ValueError("%s must be contiguous behind its tokens" % name)
+    return st[:2]
 
 
 def _flat(t, name, dtype, shape, dev):
-    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or \
+    """Check a contiguous tensor; returns its address."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != dev or \
             not t.is_contiguous():
         _need(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _opt(t, name, dtype, shape, dev):
+    """Likewise of an optional one; None stays."""
+    return None if t is None else _flat(t, name, dtype, shape, dev)
+
+
 def _checkpoint(c, name, shape, dev):
-    _flat(c.values, name + ".values", torch.float8_e4m3fn, shape, dev)
-    _flat(c.scale, name + ".scale", torch.uint8, shape[:-1], dev)
-    return c.values.data_ptr(), c.scale.data_ptr()
+    return (_flat(c.values, name + ".values", torch.float8_e4m3fn, shape, dev),
+            _flat(c.scale, name + ".scale", torch.uint8, shape[:-1], dev))
 
 
 def _new_checkpoint(shape, dev):
@@ -161,7 +173,7 @@ def pack8(x, out=None):
     prob = _pack8_problem(shape, _io_of(x), strides)
     out = out if out is not None else _new_checkpoint(shape, dev)
     c = GdnCheckpoint(*_checkpoint(out, "out", shape, dev))
-    _call(dev, "gdn_pack8", ctypes.byref(prob), x.data_ptr(), ctypes.byref(c))
+    _call(dev, lib().gdn_pack8, "gdn_pack8", ctypes.byref(prob), x.data_ptr(), ctypes.byref(c))
     return out
 
 
@@ -175,7 +187,7 @@ def unpack8(checkpoint, dtype=torch.bfloat16, out=None):
     out = out if out is not None else _empty(shape, dtype, dev)
     strides = _view(out, "out", dtype, shape, dev)
     prob = _pack8_problem(shape, _io_of(out), strides)
-    _call(dev, "gdn_unpack8", ctypes.byref(prob), ctypes.byref(c), out.data_ptr())
+    _call(dev, lib().gdn_unpack8, "gdn_unpack8", ctypes.byref(prob), ctypes.byref(c), out.data_ptr())
     return out
 
 
@@ -234,6 +246,9 @@ class QkPlan:
             self._backward_buffers()
         self._from = (GdnCheckpoint * 2)()
         self._strides = None
+        self._shared = False
+        self._inner = _inner(self.q_shape)
+        self._forward, self._backward = lib().gdn_qk_forward, lib().gdn_qk_backward
 
     def _forward_buffers(self):
         self.q_out = _empty(self.q_shape, self.dtype, self.device)
@@ -265,27 +280,26 @@ class QkPlan:
             f[0].values, f[0].scale = _checkpoint(q, "q", self.q_shape, self.device)
             f[1].values, f[1].scale = _checkpoint(k, "k", self.k_shape, self.device)
             return None, None, f, (0, 0), (0, 0)
-        qs = _view(q, "q", self.dtype, self.q_shape, self.device)
-        ks = _view(k, "k", self.dtype, self.k_shape, self.device)
+        qs = _view(q, "q", self.dtype, self.q_shape, self.device, self._inner)
+        ks = _view(k, "k", self.dtype, self.k_shape, self.device, self._inner)
         return q.data_ptr(), k.data_ptr(), None, qs, ks
 
     def _rest(self, positions, q_weight, k_weight, lengths):
-        B, L, dev = self.q_shape[0], self.q_shape[1], self.device
-        if positions is None and self.axes:
-            raise ValueError("positions are required")
+        B, L, dev, axes = self.q_shape[0], self.q_shape[1], self.device, self.axes
+        pos = None
         if positions is not None:
-            if not self.axes:
+            if not axes:
                 raise ValueError("positions without axis_pairs")
             shared = positions.dim() == 2
-            _flat(positions, "positions", torch.int32,
-                  (L, self.axes) if shared else (B, L, self.axes), dev)
-            self.prob.shared_positions = int(shared)
-        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                _flat(w, name, torch.float32, (self.D,), dev)
-        if lengths is not None:
-            _flat(lengths, "lengths", torch.int32, (B,), dev)
-        return _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(lengths)
+            pos = _flat(positions, "positions", torch.int32, (L, axes) if shared else (B, L, axes),
+                        dev)
+            if shared != self._shared:
+                self.prob.shared_positions = self._shared = shared
+        elif axes:
+            raise ValueError("positions are required")
+        return (_opt(q_weight, "q_weight", torch.float32, (self.D,), dev),
+                _opt(k_weight, "k_weight", torch.float32, (self.D,), dev), pos,
+                _opt(lengths, "lengths", torch.int32, (B,), dev))
 
     def forward(self, q, k, positions=None, q_weight=None, k_weight=None, lengths=None):
         """q and k (tensors [B, L, H, D], or their checkpoints) normalised,
@@ -299,7 +313,7 @@ class QkPlan:
         self._set_strides((qs, ks, (0, 0), (0, 0)))
         if self.q_out is None:
             self._forward_buffers()
-        _call(self.device, "gdn_qk_forward", self._ref, qp, kp, src, *rest,
+        _call(self.device, self._forward, "gdn_qk_forward", self._ref, qp, kp, src, *rest,
               self.q_out.data_ptr(), self.k_out.data_ptr(), self._to)
         return self.q_out, self.k_out
 
@@ -313,21 +327,21 @@ class QkPlan:
         dev = self.device
         qp, kp, src, qs, ks = self._source(q, k)
         rest = self._rest(positions, q_weight, k_weight, lengths)
-        _flat(d_q, "d_q", self.dtype, self.q_shape, dev)
-        _flat(d_k, "d_k", self.dtype, self.k_shape, dev)
+        d_qp = _flat(d_q, "d_q", self.dtype, self.q_shape, dev)
+        d_kp = _flat(d_k, "d_k", self.dtype, self.k_shape, dev)
         if (dq is None or dk is None or self.weights and self.dw is None) and self.dq is None:
             self._backward_buffers()
         dq, dk = self.dq if dq is None else dq, self.dk if dk is None else dk
-        dqs = _view(dq, "dq", self.dtype, self.q_shape, dev)
-        dks = _view(dk, "dk", self.dtype, self.k_shape, dev)
+        dqs = _view(dq, "dq", self.dtype, self.q_shape, dev, self._inner)
+        dks = _view(dk, "dk", self.dtype, self.k_shape, dev, self._inner)
         self._set_strides((qs, ks, dqs, dks))
         w0 = w1 = ws = None
         nws = 0
         if self.weights:
             w0 = self.dw.data_ptr()
             w1, ws, nws = w0 + 4 * self.D, self.ws.data_ptr(), self.ws.numel()
-        _call(dev, "gdn_qk_backward", self._ref, qp, kp, src, *rest, d_q.data_ptr(),
-              d_k.data_ptr(), dq.data_ptr(), dk.data_ptr(), w0, w1, ws, nws)
+        _call(dev, self._backward, "gdn_qk_backward", self._ref, qp, kp, src, *rest, d_qp, d_kp,
+              dq.data_ptr(), dk.data_ptr(), w0, w1, ws, nws)
         out = {"dq": dq, "dk": dk}
         if self.weights:
             if q_weight is not None:
@@ -420,6 +434,9 @@ class LrecPlan:
             self.dgate = _empty(self.shape, dt, dev)
             self.dstate_in = _empty(self.state_shape, torch.float32, dev)
         self._strides = None
+        self._fwd, self._bwd = lib().gdn_lrec_forward, lib().gdn_lrec_backward
+        self._o, self._saved, self._ws = _ptr(self.o), _ptr(self.saved), self.ws.data_ptr()
+        self._nws = self.ws.numel()
 
     def _set_strides(self, strides):
         if strides != self._strides:
@@ -428,28 +445,26 @@ class LrecPlan:
                 field[0], field[1] = s
             self._strides = strides
 
-    def _inputs(self, x, gate, lengths, states):
-        dev = self.device
-        xs = _view(x, "x", self.dtype, self.shape, dev)
-        gs = _view(gate, "gate", self.dtype, self.shape, dev)
-        if lengths is not None:
-            _flat(lengths, "lengths", torch.int32, self.shape[:1], dev)
-        for t, name in states:
-            if t is not None:
-                _flat(t, name, torch.float32, self.state_shape, dev)
-        return xs, gs
+    def _state(self, t, name):
+        return _opt(t, name, torch.float32, self.state_shape, self.device)
+
+    def _lengths(self, t):
+        return _opt(t, "lengths", torch.int32, self.shape[:1], self.device)
+
+    def _inputs(self, x, gate):
+        return (_view(x, "x", self.dtype, self.shape, self.device, (1,)),
+                _view(gate, "gate", self.dtype, self.shape, self.device, (1,)))
 
     def forward(self, x, gate, state=None, lengths=None, state_out=None):
         """(o, state_out) of gdn_lrec_forward.  state_out: None (the plan's
         own buffer) or a [B, C] fp32 tensor, which may be `state` itself."""
         if self.o is None:
             raise ValueError("the plan was made without forward")
-        strides = self._inputs(x, gate, lengths, ((state, "state"), (state_out, "state_out")))
-        self._set_strides(strides + ((0, 0), (0, 0)))
         so = self.state_out if state_out is None else state_out
-        _call(self.device, "gdn_lrec_forward", self._ref, x.data_ptr(), gate.data_ptr(),
-              _ptr(lengths), _ptr(state), self.o.data_ptr(), so.data_ptr(), _ptr(self.saved),
-              self.ws.data_ptr(), self.ws.numel())
+        self._set_strides(self._inputs(x, gate) + ((0, 0), (0, 0)))
+        _call(self.device, self._fwd, "gdn_lrec_forward", self._ref, x.data_ptr(),
+              gate.data_ptr(), self._lengths(lengths), self._state(state, "state"), self._o,
+              self._state(so, "state_out"), self._saved, self._ws, self._nws)
         return self.o, so
 
     def step(self, x, gate, state):
@@ -458,10 +473,9 @@ class LrecPlan:
             raise ValueError("the plan was made without forward")
         if state is None:
             raise ValueError("state is required")
-        strides = self._inputs(x, gate, None, ((state, "state"),))
-        self._set_strides(strides + ((0, 0), (0, 0)))
-        _call(self.device, "gdn_lrec_step", self._ref, x.data_ptr(), gate.data_ptr(),
-              state.data_ptr(), self.o.data_ptr())
+        self._set_strides(self._inputs(x, gate) + ((0, 0), (0, 0)))
+        _call(self.device, lib().gdn_lrec_step, "gdn_lrec_step", self._ref, x.data_ptr(),
+              gate.data_ptr(), self._state(state, "state"), self._o)
         return self.o
 
     def backward(self, x, gate, d_o, state=None, d_state=None, lengths=None, saved=None, dx=None,
@@ -472,16 +486,17 @@ class LrecPlan:
         dev = self.device
         if self.dstate_in is None:
             raise ValueError("the plan was made without backward")
-        strides = self._inputs(x, gate, lengths, ((state, "state"), (d_state, "d_state")))
-        _flat(d_o, "d_o", self.dtype, self.shape, dev)
-        if saved is not None:
+        strides = self._inputs(x, gate)
+        dp = _flat(d_o, "d_o", self.dtype, self.shape, dev)
+        saved = None if saved is None else \
             _flat(saved, "saved", torch.uint8, (lrec_saved_size(self.prob),), dev)
         dx, dgate = self.dx if dx is None else dx, self.dgate if dgate is None else dgate
-        self._set_strides(strides + (_view(dx, "dx", self.dtype, self.shape, dev),
-                                     _view(dgate, "dgate", self.dtype, self.shape, dev)))
-        _call(dev, "gdn_lrec_backward", self._ref, x.data_ptr(), gate.data_ptr(), _ptr(lengths),
-              _ptr(state), d_o.data_ptr(), _ptr(d_state), _ptr(saved), dx.data_ptr(),
-              dgate.data_ptr(), self.dstate_in.data_ptr(), self.ws.data_ptr(), self.ws.numel())
+        self._set_strides(strides + (_view(dx, "dx", self.dtype, self.shape, dev, (1,)),
+                                     _view(dgate, "dgate", self.dtype, self.shape, dev, (1,))))
+        _call(dev, self._bwd, "gdn_lrec_backward", self._ref, x.data_ptr(), gate.data_ptr(),
+              self._lengths(lengths), self._state(state, "state"), dp,
+              self._state(d_state, "d_state"), saved, dx.data_ptr(), dgate.data_ptr(),
+              self.dstate_in.data_ptr(), self._ws, self._nws)
         return {"dx": dx, "dgate": dgate, "dstate_in": self.dstate_in}
 
 
