@@ -26,8 +26,7 @@ namespace gdn {
 
 constexpr int kTokens = 16;                 // tokens of a wave
 constexpr int kGroup = kLrecGroup;
-constexpr int kLrecWaves = kLrecChunk / kTokens;
-constexpr int kLrecThreads = 64 * kLrecWaves;
+constexpr int kLrecWaves = kLrecChunk / kTokens;   // a workgroup's, 1 for up to kTokens tokens
 static_assert(kGroup <= kLrecWaves, "a wave for each earlier chunk of a group and one for its state");
 
 // VEC io elements as loaded (bf16: one or two, fp32: one; a word either way),
@@ -51,7 +50,7 @@ __device__ __forceinline__ void vec_store(void* p, const float* f) {
   if constexpr (IO == IO_F32) *reinterpret_cast<float*>(p) = f[0];
   else if constexpr (VEC == 2)
     *reinterpret_cast<uint32_t*>(p) =
-        (uint32_t)f32_to_bf16_bits(f[0]) | ((uint32_t)f32_to_bf16_bits(f[1]) << 16);
+        __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{f[0], f[1]}), bf16x2));
   else *reinterpret_cast<uint16_t*>(p) = f32_to_bf16_bits(f[0]);
 }
 
@@ -102,7 +101,8 @@ __device__ __forceinline__ int length_of(const LrecArgs& p, int b) {
 
 // Where a workgroup and its wave stand.
 struct Tile {
-  int b, step, chunk;   // step: the chunk's turn (backwards: from the end)
+  int b, step, chunk;   // step: the chunk's turn in its sequence (backwards: from its end)
+  bool last, dead;      // the last step; behind the sequence's end altogether
   int t0, live;         // the wave's first token, its tokens before the sequence's end
   int c0;               // the strip's first channel
   int cl;               // the lane's first channel from there, of one that exists
@@ -118,13 +118,17 @@ __device__ __forceinline__ Tile tile_at(const LrecArgs& p) {
     id = __builtin_amdgcn_readfirstlane(drawn);
   }
   Tile t;
-  const unsigned per = (unsigned)p.B * p.strips;
-  t.step = id / per;
-  t.chunk = REVERSE ? p.chunks - 1 - t.step : t.step;
-  const unsigned r = id - t.step * per;
+  const unsigned per = (unsigned)p.B * p.strips, turn = id / per, r = id - turn * per;
+  t.chunk = REVERSE ? p.chunks - 1 - turn : turn;
   t.b = r / (unsigned)p.strips;
   t.t0 = t.chunk * kLrecChunk + wave_id() * kTokens;
-  t.live = length_of(p, t.b) - t.t0;
+  const int len = length_of(p, t.b);
+  t.live = len - t.t0;
+  // a sequence has the chunks that its tokens reach, the first in any case
+  const int own = len > 0 ? (len - 1) / kLrecChunk + 1 : 1;
+  t.dead = t.chunk >= own;
+  t.step = REVERSE ? own - 1 - t.chunk : t.chunk;
+  t.last = t.step == own - 1;
   t.c0 = (r - t.b * p.strips) * 64 * VEC;
   t.in = t.c0 + lane_id() * VEC < p.C;
   t.cl = t.in ? lane_id() * VEC : 0;
@@ -132,9 +136,9 @@ __device__ __forceinline__ Tile tile_at(const LrecArgs& p) {
 }
 
 // Maps (A, H) of a chunk's waves or of a group's chunks, [index][64 VEC].
-template <int VEC>
+template <int VEC, int WAVES>
 struct Maps {
-  float A[kLrecWaves][64 * VEC], H[kLrecWaves][64 * VEC];
+  float A[WAVES][64 * VEC], H[WAVES][64 * VEC];
 };
 
 constexpr uint32_t kUnset = 0xffffffffu;
@@ -143,61 +147,72 @@ __device__ __forceinline__ uint32_t publishable(float f) {
   return u == kUnset ? 0x7fc00000u : u;   // a NaN either way
 }
 
-// The state entering the chunk, in h: `maps` holds the maps of the chunk's
-// waves (barrier passed), in the order `first`, `first + dir`, ...  `initial`
-// is the sequence's [B, C] or nullptr.
-template <int VEC, bool REVERSE>
+// What the workgroup's waves share of the state entering its chunk.
+template <int VEC, int WAVES>
+struct Entering {
+  Maps<VEC, WAVES> before;   // maps of the group's earlier chunks
+  float start[64 * VEC];     // the state entering the group
+};
+
+// First part, before the barrier that the chunk's maps take: a group's start
+// that is the sequence's own (`initial`, [B, C] or nullptr).  Nothing of the
+// chunk is published until this read is done, and the sequence's last chunk
+// cannot end before everything before it is published: it may write its state
+// over `initial`.
+template <int VEC, int WAVES>
+__device__ __forceinline__ void first_state(const LrecArgs& p, const Tile& t, const float* initial,
+                                            Entering<VEC, WAVES>& s) {
+  if (wave_id() != WAVES - 1 || t.step >= kGroup) return;
+  const int64_t bc = (int64_t)t.b * p.C + t.c0 + t.cl;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    s.start[lane_id() * VEC + e] = initial ? initial[bc + e] : 0.f;
+}
+
+// Second part, behind it: the state in h.  `maps` are those of the chunk's
+// waves, in the order of the waves or the reverse.
+template <int VEC, int WAVES, bool REVERSE>
 __device__ __forceinline__ void entering_state(const LrecArgs& p, const Tile& t,
-                                               const Maps<VEC>& maps, const float* initial,
-                                               float* h) {
+                                               const Maps<VEC, WAVES>& maps,
+                                               Entering<VEC, WAVES>& s, float* h) {
   const int w = wave_id(), col = lane_id() * VEC;
   const int64_t BC = (int64_t)p.B * p.C, bc = (int64_t)t.b * p.C + t.c0 + t.cl;
-  if (p.chunks == 1) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = initial ? initial[bc + e] : 0.f;
-    return;
-  }
-  __shared__ Maps<VEC> before;
-  __shared__ float start[64 * VEC];
   const int g = t.step / kGroup, r = t.step % kGroup;
-  const bool last = t.step == p.chunks - 1;
-  if (w == 0 && t.in && r != kGroup - 1 && !last) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float A = 1.f, H = 0.f;
-#pragma unroll
-      for (int k = 0; k < kLrecWaves; ++k) {
-        const int v = REVERSE ? kLrecWaves - 1 - k : k;
-        H = fmaf(maps.A[v][col + e], H, maps.H[v][col + e]);
-        A *= maps.A[v][col + e];
-      }
-      __hip_atomic_store(p.agg + (int64_t)t.step * BC + bc + e,
-                         (uint64_t)publishable(A) | (uint64_t)__float_as_uint(H) << 32,
-                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-  }
-  if (w < r) {
-    const uint64_t* from = p.agg + (int64_t)(t.step - r + w) * BC + bc;
-    uint64_t v[VEC];
-    bool there;
-    do {
-      there = true;
+  const bool several = WAVES > 1 && p.chunks > 1;
+  if (several) {
+    if (w == 0 && t.in && r != kGroup - 1 && !t.last) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        v[e] = __hip_atomic_load(from + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        there = there && (uint32_t)v[e] != kUnset;
+        float A = 1.f, H = 0.f;
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) {
+          const int v = REVERSE ? WAVES - 1 - k : k;
+          H = fmaf(maps.A[v][col + e], H, maps.H[v][col + e]);
+          A *= maps.A[v][col + e];
+        }
+        __hip_atomic_store(p.agg + (int64_t)t.step * BC + bc + e,
+                           (uint64_t)publishable(A) | (uint64_t)__float_as_uint(H) << 32,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-    } while (!__all(there || !t.in));
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      before.A[w][col + e] = __uint_as_float((uint32_t)v[e]);
-      before.H[w][col + e] = __uint_as_float((uint32_t)(v[e] >> 32));
     }
-  } else if (w == kLrecWaves - 1) {
-    if (g == 0) {
+    if (w < r) {
+      const uint64_t* from = p.agg + (int64_t)(t.step - r + w) * BC + bc;
+      uint64_t v[VEC];
+      bool there;
+      do {
+        there = true;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) start[col + e] = initial ? initial[bc + e] : 0.f;
-    } else {
+        for (int e = 0; e < VEC; ++e) {
+          v[e] = __hip_atomic_load(from + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          there = there && (uint32_t)v[e] != kUnset;
+        }
+      } while (!__all(there || !t.in));
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        s.before.A[w][col + e] = __uint_as_float((uint32_t)v[e]);
+        s.before.H[w][col + e] = __uint_as_float((uint32_t)(v[e] >> 32));
+      }
+    } else if (w == WAVES - 1 && g > 0) {
       const uint32_t* from = p.pre + (int64_t)(g - 1) * BC + bc;
       uint32_t v[VEC];
       bool there;
@@ -210,22 +225,24 @@ __device__ __forceinline__ void entering_state(const LrecArgs& p, const Tile& t,
         }
       } while (!__all(there || !t.in));
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) start[col + e] = __uint_as_float(v[e]);
+      for (int e = 0; e < VEC; ++e) s.start[col + e] = __uint_as_float(v[e]);
     }
+    __syncthreads();
   }
-  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) h[e] = start[col + e];
+  for (int e = 0; e < VEC; ++e) h[e] = s.start[col + e];
+  if (!several) return;
   for (int k = 0; k < r; ++k)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = fmaf(before.A[k][col + e], h[e], before.H[k][col + e]);
-  if (w == 0 && t.in && r == kGroup - 1 && !last) {
+    for (int e = 0; e < VEC; ++e)
+      h[e] = fmaf(s.before.A[k][col + e], h[e], s.before.H[k][col + e]);
+  if (w == 0 && t.in && r == kGroup - 1 && !t.last) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       float n = h[e];
 #pragma unroll
-      for (int k = 0; k < kLrecWaves; ++k) {
-        const int v = REVERSE ? kLrecWaves - 1 - k : k;
+      for (int k = 0; k < WAVES; ++k) {
+        const int v = REVERSE ? WAVES - 1 - k : k;
         n = fmaf(maps.A[v][col + e], n, maps.H[v][col + e]);
       }
       __hip_atomic_store(p.pre + (int64_t)g * BC + bc + e, publishable(n), __ATOMIC_RELAXED,
@@ -253,46 +270,57 @@ __device__ __forceinline__ float* state_row(const LrecArgs& p, const Tile& t, fl
 }
 
 // The wave's tokens of one tensor, row by row at stride `sl` elements; rows
-// behind the sequence's end read its last row again (`dead` replaces what was
-// read), a wave without a row reads nothing.
+// behind the sequence's end are not read (`dead` stands for them).
 template <int IO, int VEC>
 __device__ __forceinline__ void load_tokens(const Tile& t, const void* base, int64_t sb,
                                             int64_t sl, uint32_t dead, Vec<IO, VEC>* v) {
-  if (t.live <= 0) {
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) v[i].fill(dead);
-    return;
-  }
   const char* row = wave_row<IO>(t, base, sb, sl);
   const uint32_t off = t.cl * Io<IO>::bytes;
-  const int end = t.live - 1;
+  const int64_t step = sl * Io<IO>::bytes;
+  if (t.live >= kTokens) {
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i)
-    v[i].load(row + (i < end ? i : end) * sl * Io<IO>::bytes + off);
-  if (t.live < kTokens) {
+    for (int i = 0; i < kTokens; ++i, row += step) v[i].load(row + off);
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i)
-      if (i >= t.live) v[i].fill(dead);
+  for (int i = 0; i < kTokens; ++i, row += step) {
+    if (i < t.live) v[i].load(row + off);
+    else v[i].fill(dead);
   }
 }
 
+// Zeros in the wave's tokens of an output.
+template <int IO, int VEC>
+__device__ __forceinline__ void clear_tokens(const LrecArgs& p, const Tile& t, void* base,
+                                             int64_t sb, int64_t sl) {
+  const float zero[2] = {0.f, 0.f};
+  char* row = wave_row<IO>(t, base, sb, sl);
+  for (int i = 0; i < kTokens && t.t0 + i < p.L; ++i, row += sl * Io<IO>::bytes)
+    if (t.in) vec_store<IO, VEC>(row + t.cl * Io<IO>::bytes, zero);
+}
+
 // STATES: only the states entering the chunks (enter), else the outputs too.
-template <int IO, int VEC, bool LOGITS, bool STATES>
-__global__ __launch_bounds__(kLrecThreads) void lrec_forward_kernel(LrecArgs p) {
+template <int IO, int VEC, int WAVES, bool LOGITS, bool STATES>
+__global__ __launch_bounds__(64 * WAVES) void lrec_forward_kernel(LrecArgs p) {
   constexpr int ES = Io<IO>::bytes;
-  __shared__ Maps<VEC> maps;
+  __shared__ Maps<VEC, WAVES> maps;
+  __shared__ Entering<VEC, WAVES> entering;
   const Tile t = tile_at<VEC, false>(p);
+  if (t.dead) {
+    if constexpr (!STATES) clear_tokens<IO, VEC>(p, t, p.o, (int64_t)p.L * p.C, p.C);
+    return;
+  }
   const int w = wave_id(), col = lane_id() * VEC;
   float a[kTokens][VEC], u[kTokens][VEC];
   {
     Vec<IO, VEC> x[kTokens], z[kTokens];
     load_tokens<IO, VEC>(t, p.z, p.z_sb, p.z_sl, open_word<IO, LOGITS>(), z);
     load_tokens<IO, VEC>(t, p.x, p.x_sb, p.x_sl, 0u, x);
+    first_state<VEC, WAVES>(p, t, p.h0, entering);
     float A[VEC], H[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) A[e] = 1.f, H[e] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
+    auto token = [&](int i) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float v = gate_keep<IO, LOGITS>(z[i].get(e));
@@ -300,6 +328,20 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_forward_kernel(LrecArgs p) 
         u[i][e] = x[i].get(e) * (p.complement ? gate_na<LOGITS>(v) : 1.f);
         A[e] *= a[i][e];
         H[e] = fmaf(a[i][e], H[e], u[i][e]);
+      }
+    };
+    if (t.live >= kTokens) {
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) token(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) {
+        if (i < t.live) {
+          token(i);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) a[i][e] = 1.f, u[i][e] = 0.f;
+        }
       }
     }
 #pragma unroll
@@ -310,7 +352,7 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_forward_kernel(LrecArgs p) 
   }
   __syncthreads();
   float h[VEC];
-  entering_state<VEC, false>(p, t, maps, p.h0, h);
+  entering_state<VEC, WAVES, false>(p, t, maps, entering, h);
   if (!t.in) return;
   if (p.enter && w == 0) {
     float* q = state_row(p, t, p.enter, p.chunks, t.chunk);
@@ -321,20 +363,29 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_forward_kernel(LrecArgs p) 
   for (int k = 0; k < w; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) h[e] = fmaf(maps.A[k][col + e], h[e], maps.H[k][col + e]);
-  char* op = wave_row<IO>(t, p.o, (int64_t)p.L * p.C, p.C);
+  char* row = wave_row<IO>(t, p.o, (int64_t)p.L * p.C, p.C);
   const uint32_t off = t.cl * ES;
-  const int rows = p.L - t.t0;
+  const int64_t step = (int64_t)p.C * ES;
+  if (t.live >= kTokens) {
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
-    float o[VEC];
+    for (int i = 0; i < kTokens; ++i, row += step) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      h[e] = fmaf(a[i][e], h[e], u[i][e]);
-      o[e] = i < t.live ? h[e] : 0.f;
+      for (int e = 0; e < VEC; ++e) h[e] = fmaf(a[i][e], h[e], u[i][e]);
+      vec_store<IO, VEC>(row + off, h);
     }
-    if (i < rows) vec_store<IO, VEC>(op + (int64_t)i * p.C * ES + off, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i, row += step) {
+      float o[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        h[e] = fmaf(a[i][e], h[e], u[i][e]);
+        o[e] = i < t.live ? h[e] : 0.f;
+      }
+      if (t.t0 + i < p.L) vec_store<IO, VEC>(row + off, o);
+    }
   }
-  if (p.hT && t.chunk == p.chunks - 1 && w == kLrecWaves - 1) {
+  if (p.hT && t.last && w == WAVES - 1) {
     float* q = state_row(p, t, p.hT, 1, 0);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) q[t.cl + e] = h[e];
@@ -349,11 +400,17 @@ __device__ __forceinline__ void formed_again(float& f) { asm volatile("" : "+v"(
 __device__ __forceinline__ void formed_again(uint32_t& u) { asm volatile("" : "+v"(u)); }
 
 // The gradients; the states entering the chunks are in enter.
-template <int IO, int VEC, bool LOGITS>
-__global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p) {
+template <int IO, int VEC, int WAVES, bool LOGITS>
+__global__ __launch_bounds__(64 * WAVES) void lrec_backward_kernel(LrecArgs p) {
   constexpr int ES = Io<IO>::bytes;
-  __shared__ Maps<VEC> back, fore;
+  __shared__ Maps<VEC, WAVES> back, fore;
+  __shared__ Entering<VEC, WAVES> entering;
   const Tile t = tile_at<VEC, true>(p);
+  if (t.dead) {
+    clear_tokens<IO, VEC>(p, t, p.dx, p.dx_sb, p.dx_sl);
+    clear_tokens<IO, VEC>(p, t, p.dz, p.dz_sb, p.dz_sl);
+    return;
+  }
   const int w = wave_id(), col = lane_id() * VEC;
   Vec<IO, VEC> x[kTokens], d[kTokens];
   float v[kTokens][VEC];
@@ -363,6 +420,7 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p)
     load_tokens<IO, VEC>(t, p.z, p.z_sb, p.z_sl, open_word<IO, LOGITS>(), z);
     load_tokens<IO, VEC>(t, p.d_o, (int64_t)p.L * p.C, p.C, 0u, d);
     load_tokens<IO, VEC>(t, p.x, p.x_sb, p.x_sl, 0u, x);
+    first_state<VEC, WAVES>(p, t, p.dhT, entering);
     const float* q = state_row(p, t, p.enter, p.chunks, t.chunk);
     float A[VEC], H[VEC];
 #pragma unroll
@@ -389,7 +447,7 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p)
   }
   __syncthreads();
   float c[VEC];
-  entering_state<VEC, true>(p, t, back, p.dhT, c);
+  entering_state<VEC, WAVES, true>(p, t, back, entering, c);
   if (!t.in) return;
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
@@ -401,7 +459,7 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p)
   for (int k = 0; k < w; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) h[e] = fmaf(fore.A[k][col + e], h[e], fore.H[k][col + e]);
-  for (int k = kLrecWaves - 1; k > w; --k)
+  for (int k = WAVES - 1; k > w; --k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) c[e] = fmaf(back.A[k][col + e], c[e], back.H[k][col + e]);
   float f[kTokens][VEC];   // h_{l-1} [- x_l]: the factor of da
@@ -419,25 +477,42 @@ __global__ __launch_bounds__(kLrecThreads) void lrec_backward_kernel(LrecArgs p)
   for (int i = 0; i < kTokens; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) formed_again(v[i][e]);
-  char* dxp = wave_row<IO>(t, p.dx, p.dx_sb, p.dx_sl);
-  char* dzp = wave_row<IO>(t, p.dz, p.dz_sb, p.dz_sl);
   const uint32_t off = t.cl * ES;
-  const int rows = p.L - t.t0;
-#pragma unroll
-  for (int i = kTokens - 1; i >= 0; --i) {
-    float dx[VEC], dz[VEC];
+  const int64_t xstep = p.dx_sl * ES, zstep = p.dz_sl * ES;
+  char* xrow = wave_row<IO>(t, p.dx, p.dx_sb, p.dx_sl) + (kTokens - 1) * xstep;
+  char* zrow = wave_row<IO>(t, p.dz, p.dz_sb, p.dz_sl) + (kTokens - 1) * zstep;
+  auto token = [&](int i, float* dx, float* dz) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float a = gate_a<LOGITS>(v[i][e]), na = gate_na<LOGITS>(v[i][e]);
       const float G = d[i].get(e) + c[e];
       const float da = G * f[i][e];
-      dz[e] = i < t.live ? (LOGITS ? da * (a * na) : da) : 0.f;
-      dx[e] = i < t.live ? (p.complement ? G * na : G) : 0.f;
+      dz[e] = LOGITS ? da * (a * na) : da;
+      dx[e] = p.complement ? G * na : G;
       c[e] = a * G;
     }
-    if (i < rows) {
-      vec_store<IO, VEC>(dxp + i * p.dx_sl * ES + off, dx);
-      vec_store<IO, VEC>(dzp + i * p.dz_sl * ES + off, dz);
+  };
+  if (t.live >= kTokens) {
+#pragma unroll
+    for (int i = kTokens - 1; i >= 0; --i, xrow -= xstep, zrow -= zstep) {
+      float dx[VEC], dz[VEC];
+      token(i, dx, dz);
+      vec_store<IO, VEC>(xrow + off, dx);
+      vec_store<IO, VEC>(zrow + off, dz);
+    }
+  } else {
+#pragma unroll
+    for (int i = kTokens - 1; i >= 0; --i, xrow -= xstep, zrow -= zstep) {
+      float dx[VEC], dz[VEC];
+      token(i, dx, dz);
+      if (i >= t.live) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dx[e] = dz[e] = 0.f;
+      }
+      if (t.t0 + i < p.L) {
+        vec_store<IO, VEC>(xrow + off, dx);
+        vec_store<IO, VEC>(zrow + off, dz);
+      }
     }
   }
   if (p.dh0 && t.chunk == 0 && w == 0) {
@@ -465,40 +540,45 @@ static void clear(const LrecArgs& p, hipStream_t s) {
 
 template <int IO, int VEC, bool LOGITS>
 static hipError_t forward_as(const LrecArgs& p, bool states, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(kLrecThreads);
+  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(64 * kLrecWaves);
   if (p.chunks > 1) clear(p, s);
-  if (states) hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, true>), g, t, 0, s, p);
-  else hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, LOGITS, false>), g, t, 0, s, p);
+  if (states)
+    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, kLrecWaves, LOGITS, true>), g, t, 0, s, p);
+  else if (p.L <= kTokens)
+    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, 1, LOGITS, false>), g, dim3(64), 0, s, p);
+  else
+    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, kLrecWaves, LOGITS, false>), g, t, 0, s, p);
   return hipGetLastError();
 }
 
 template <int IO, int VEC, bool LOGITS>
 static hipError_t backward_as(const LrecArgs& p, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(kLrecThreads);
+  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(64 * kLrecWaves);
   if (p.chunks > 1) clear(p, s);
-  hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, LOGITS>), g, t, 0, s, p);
+  if (p.L <= kTokens)
+    hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, 1, LOGITS>), g, dim3(64), 0, s, p);
+  else
+    hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, kLrecWaves, LOGITS>), g, t, 0, s, p);
   return hipGetLastError();
 }
 
+template <int IO, int VEC>
+static hipError_t forward_gates(const LrecArgs& p, bool states, hipStream_t s) {
+  return p.logits ? forward_as<IO, VEC, true>(p, states, s)
+                  : forward_as<IO, VEC, false>(p, states, s);
+}
 hipError_t launch_lrec_forward(const LrecArgs& p, int io, int vec, bool states, hipStream_t s) {
-  if (io == IO_BF16) {
-    if (vec == 2)
-      return p.logits ? forward_as<IO_BF16, 2, true>(p, states, s)
-                      : forward_as<IO_BF16, 2, false>(p, states, s);
-    return p.logits ? forward_as<IO_BF16, 1, true>(p, states, s)
-                    : forward_as<IO_BF16, 1, false>(p, states, s);
-  }
-  return p.logits ? forward_as<IO_F32, 1, true>(p, states, s)
-                  : forward_as<IO_F32, 1, false>(p, states, s);
+  if (io == IO_F32) return forward_gates<IO_F32, 1>(p, states, s);
+  return vec == 2 ? forward_gates<IO_BF16, 2>(p, states, s) : forward_gates<IO_BF16, 1>(p, states, s);
 }
 
+template <int IO, int VEC>
+static hipError_t backward_gates(const LrecArgs& p, hipStream_t s) {
+  return p.logits ? backward_as<IO, VEC, true>(p, s) : backward_as<IO, VEC, false>(p, s);
+}
 hipError_t launch_lrec_backward(const LrecArgs& p, int io, int vec, hipStream_t s) {
-  if (io == IO_BF16) {
-    if (vec == 2)
-      return p.logits ? backward_as<IO_BF16, 2, true>(p, s) : backward_as<IO_BF16, 2, false>(p, s);
-    return p.logits ? backward_as<IO_BF16, 1, true>(p, s) : backward_as<IO_BF16, 1, false>(p, s);
-  }
-  return p.logits ? backward_as<IO_F32, 1, true>(p, s) : backward_as<IO_F32, 1, false>(p, s);
+  if (io == IO_F32) return backward_gates<IO_F32, 1>(p, s);
+  return vec == 2 ? backward_gates<IO_BF16, 2>(p, s) : backward_gates<IO_BF16, 1>(p, s);
 }
 
 }  // namespace gdn

@@ -188,6 +188,22 @@ def test_steps_and_windows_equal_one_call(io):
     close(state, rh, eh, "fp32", "state of the windows")
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,L,C", [(40, 1, 700), (8, 16, 700), (8, 100, 700), (4, 129, 1400),
+                                   (4, 900, 1400), (2, 3000, 1400)])
+def test_state_in_place_equals_state_apart(B, L, C, io):
+    # the last chunk writes its state over the one that the first chunks read
+    c = case(B, L, C, io, True, seed=14)
+    x, z, h0 = on(c["x"]), on(c["z"]), on(c["h0"])
+    plan = block.LrecPlan(B, L, C, io, DEV, True, True)
+    o, h = plan.forward(x, z, h0)
+    o, h = o.clone(), h.clone()
+    for _ in range(10):
+        state = h0.clone()
+        o2, _ = plan.forward(x, z, state, state_out=state)
+        assert torch.equal(o2, o) and torch.equal(state, h)
+
+
 def test_same_bits_every_time_on_any_stream():
     B, L, C = 2, 5000, 700
     c = case(B, L, C, "bf16", True, seed=7)
