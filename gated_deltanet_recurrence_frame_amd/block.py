@@ -15,6 +15,7 @@ batches and tokens at any stride.
 
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -158,7 +159,9 @@ def _new_checkpoint(shape, dev):
 
 # ---- 8-bit checkpoints --------------------------------------------------
 
+@functools.lru_cache(maxsize=256)
 def _pack8_problem(shape, io, strides):
+    """gdn_pack8_problem (only read, so one object serves equal calls)."""
     B, L, H, D = shape
     return GdnPack8Problem(B, L, H, D, GDN_BF16 if io == "bf16" else GDN_FP32, 0,
                            _Pair(*strides))
@@ -168,11 +171,13 @@ def pack8(x, out=None):
     """Checkpoint of x [B, L, H, D] (bf16 or fp32; gdn_pack8)."""
     if x.dim() != 4:
         raise ValueError("x must be [B, L, H, D]")
-    shape, dev = tuple(x.shape), x.device
-    strides = _view(x, "x", x.dtype, shape, dev)
-    prob = _pack8_problem(shape, _io_of(x), strides)
-    out = out if out is not None else _new_checkpoint(shape, dev)
-    c = GdnCheckpoint(*_checkpoint(out, "out", shape, dev))
+    shape, dev = x.shape, x.device
+    prob = _pack8_problem(shape, _io_of(x), _view(x, "x", x.dtype, shape, dev))
+    if out is None:
+        out = _new_checkpoint(shape, dev)
+        c = GdnCheckpoint(out.values.data_ptr(), out.scale.data_ptr())
+    else:
+        c = GdnCheckpoint(*_checkpoint(out, "out", shape, dev))
     _call(dev, lib().gdn_pack8, "gdn_pack8", ctypes.byref(prob), x.data_ptr(), ctypes.byref(c))
     return out
 
@@ -182,12 +187,12 @@ def unpack8(checkpoint, dtype=torch.bfloat16, out=None):
     v = checkpoint.values
     if v.dim() != 4:
         raise ValueError("checkpoint values must be [B, L, H, D]")
-    shape, dev = tuple(v.shape), v.device
+    shape, dev = v.shape, v.device
     c = GdnCheckpoint(*_checkpoint(checkpoint, "checkpoint", shape, dev))
     out = out if out is not None else _empty(shape, dtype, dev)
-    strides = _view(out, "out", dtype, shape, dev)
-    prob = _pack8_problem(shape, _io_of(out), strides)
-    _call(dev, lib().gdn_unpack8, "gdn_unpack8", ctypes.byref(prob), ctypes.byref(c), out.data_ptr())
+    prob = _pack8_problem(shape, _io_of(out), _view(out, "out", dtype, shape, dev))
+    _call(dev, lib().gdn_unpack8, "gdn_unpack8", ctypes.byref(prob), ctypes.byref(c),
+          out.data_ptr())
     return out
 
 

@@ -49,7 +49,7 @@ def ckpt(i):
 # ---- pack8 ----
 
 def pack(lib, over=None, x=at(0), values=at(1), scale=at(2), unpack=False):
-    p = block._pack8_problem((2, 3, 4, 112), "bf16", (3 * 448, 448))
+    p = block.GdnPack8Problem(2, 3, 4, 112, gb.GDN_BF16, 0, (3 * 448, 448))
     for k, v in (over or {}).items():
         if k == "stride":
             p.stride[0], p.stride[1] = v
