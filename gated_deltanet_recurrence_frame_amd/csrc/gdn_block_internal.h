@@ -53,6 +53,7 @@ struct QkArgs {
   RowShape row;
   int norm, adjacent, axes, pairs, bound1, bound2;   // pairs of axes 0, of 0 and 1
   int split;               // workgroups on the first operand, the rest on the second
+  int at_once[2];          // tokens of a wave side by side, for each operand
   int pos_shared;
   float eps, c;
   // turns (angle / 2 pi) per unit of position of every pair

@@ -16,6 +16,10 @@
 // accesses are whole rows; the partners of its elements are in the piece
 // itself (adjacent pairs) or in another lane's (halves), which it gets as
 // loaded, through the LDS crossbar.
+//
+// An operand of few heads leaves lanes without a row: a wave then takes
+// several tokens side by side (MULTI; as many, a power of two, as leave their
+// heads room in a step: tokens_at_once).
 #include "gdn_rows.h"
 
 namespace gdn {
@@ -26,55 +30,81 @@ constexpr int kRows = 2;            // rows of a lane in a step (forward)
 constexpr int kBackRows = 2;        // (backward)
 constexpr int kAhead = 2;           // steps loaded ahead (forward)
 constexpr int kBackAhead = 1;       // (backward)
-// Workgroups at most: as many as the card holds at once (256 CUs, 4 SIMDs
-// with one wave of a workgroup each) at the waves a SIMD that the registers
-// are bounded for; one more would run alone at the end.
-constexpr int kWavesPerSimd = 4, kBackWavesPerSimd = 4;
+// Waves a SIMD that the registers are bounded for, and with them workgroups at
+// most: as many as the card holds at once (256 CUs, 4 SIMDs with one wave of a
+// workgroup each); one more would run alone at the end.
+constexpr int kWavesPerSimd = 4;
+constexpr int back_waves_per_simd(bool multi) { return multi ? 3 : 4; }
 constexpr int kQkWgs = 256 * kWavesPerSimd;
-constexpr int kQkBackWgs = 256 * kBackWavesPerSimd;
+constexpr int back_wgs(bool multi) { return 256 * back_waves_per_simd(multi); }
 constexpr int kMaxPairs = kRowMaxD / 2;
 
-// Where a wave stands: a token, and a step of its rows.  The same for all
-// lanes.
+// Where a wave stands: its first token, the lane's token (the same one without
+// MULTI, the last where the wave's reach past it), and a step of its rows.
 struct Cursor {
-  uint32_t tok, b, l;
+  uint32_t tok0, tok, b, l;
   int step;
-  bool live;       // before the sequence's end
+  bool live;       // the lane's token is before its sequence's end
+  bool there;      // and not past the last
 };
-__device__ __forceinline__ void set_token(const QkArgs& a, Cursor* c, uint32_t tok) {
-  c->tok = tok;
+template <bool MULTI>
+__device__ __forceinline__ void set_token(const QkArgs& a, Cursor* c, uint32_t tok0, int tau) {
+  const uint32_t tokens = (uint32_t)a.B * a.L;
+  c->tok0 = c->tok = tok0;
   c->step = 0;
-  c->b = a.B == 1 ? 0u : tok / (uint32_t)a.L;
-  c->l = tok - c->b * (uint32_t)a.L;
-  c->live = !a.len || tok >= (uint32_t)a.B * a.L || (int)c->l < a.len[c->b];
-}
-__device__ __forceinline__ void advance(const QkArgs& a, Cursor* c, int steps, uint32_t waves) {
-  if (++c->step == steps) set_token(a, c, c->tok + waves);
+  c->there = true;
+  if constexpr (MULTI) {
+    c->tok = tok0 + tau;
+    c->there = c->tok < tokens;
+    c->tok = c->there ? c->tok : tokens - 1;
+  }
+  c->b = a.B == 1 ? 0u : c->tok / (uint32_t)a.L;
+  c->l = c->tok - c->b * (uint32_t)a.L;
+  c->live = !a.len || c->tok >= tokens || (int)c->l < a.len[c->b];
 }
 
-// A lane's share of the rotation: one pair (two in heads beyond 128).
+// A lane's share of the rotation: some pairs of the wave's tokens.
+template <int V, bool MULTI>
 struct Turns {
-  double per[2];   // turns per unit of position
-  int axis[2];
-  int pos[2];      // of the token to come
-};
-__device__ __forceinline__ void turns_init(const QkArgs& a, Turns* t) {
+  // two pairs of one token (heads beyond 128); or of 64 / group tokens and
+  // group V / 2 pairs at most
+  static constexpr int kItems = MULTI ? V / 2 : 2;
+  static constexpr int kPairs = MULTI ? 32 * V : kMaxPairs;   // of a wave in LDS
+  double per[MULTI ? 1 : kItems];   // turns per unit of position (MULTI: read each time)
+  int what[kItems];     // pair, axis << 8, the token from the wave's first << 16
+  int pos[kItems];      // of the tokens to come
+  int items;
+
+  __device__ __forceinline__ void init(const QkArgs& a, int at_once) {
+    items = a.pairs * at_once;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = lane_id() + 64 * i;
-    t->per[i] = m < a.pairs ? a.turns[m] : 0.0;
-    t->axis[i] = m < a.bound1 ? 0 : m < a.bound2 ? 1 : 2;
-    t->pos[i] = 0;
+    for (int i = 0; i < kItems; ++i) {
+      const int m = lane_id() + 64 * i;
+      const int tau = MULTI && m < items ? m / a.pairs : 0;
+      const int pair = m < items ? m - tau * a.pairs : 0;
+      what[i] = pair | (pair < a.bound1 ? 0 : pair < a.bound2 ? 1 : 2) << 8 | tau << 16;
+      if constexpr (!MULTI) per[i] = a.turns[pair];
+      pos[i] = 0;
+    }
   }
-}
-__device__ __forceinline__ void turns_fetch(const QkArgs& a, Turns* t, uint32_t tok) {
-  if (tok >= (uint32_t)a.B * a.L) return;
-  const uint32_t row = a.pos_shared ? tok % (uint32_t)a.L : tok;
-  const int32_t* pos = a.pos + (int64_t)row * a.axes;
+  __device__ __forceinline__ void fetch(const QkArgs& a, uint32_t tok0) {
+    const uint32_t tokens = (uint32_t)a.B * a.L;
+    if (tok0 >= tokens) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (lane_id() + 64 * i < a.pairs) t->pos[i] = pos[t->axis[i]];
-}
+    for (int i = 0; i < kItems; ++i) {
+      uint32_t row = tok0;
+      if constexpr (MULTI) {
+        row = tok0 + (what[i] >> 16);
+        row = row < tokens ? row : tokens - 1;
+      }
+      if (a.pos_shared) row %= (uint32_t)a.L;
+      if (lane_id() + 64 * i < items)
+        pos[i] = a.pos[(int64_t)row * a.axes + ((what[i] >> 8) & 255)];
+    }
+  }
+  // cosine and sine of item m to trig[2 m], trig[2 m + 1]
+  __device__ __forceinline__ void form(const QkArgs& a, float* trig) const;
+};
 
 // LDS written by a wave's lanes and read by others of the same wave.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -83,14 +113,14 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// trig[2 m], trig[2 m + 1]: cosine and sine of pair m.
-__device__ __forceinline__ void token_turns(const QkArgs& a, const Turns& t, float* trig) {
-  wave_lds_sync();   // the last token's reads are done
+template <int V, bool MULTI>
+__device__ __forceinline__ void Turns<V, MULTI>::form(const QkArgs& a, float* trig) const {
+  wave_lds_sync();   // the last tokens' reads are done
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kItems; ++i) {
     const int m = lane_id() + 64 * i;
-    if (m < a.pairs) {
-      double turn = (double)t.pos[i] * t.per[i];
+    if (m < items) {
+      double turn = (double)pos[i] * (MULTI ? a.turns[what[i] & 255] : per[MULTI ? 0 : i]);
       turn -= rint(turn);
       *reinterpret_cast<f32x2*>(trig + 2 * m) =
           f32x2{__builtin_amdgcn_cosf((float)turn), __builtin_amdgcn_sinf((float)turn)};
@@ -106,12 +136,14 @@ __device__ __forceinline__ float row_inverse(float ss) {
 }
 
 // What a workgroup is on: an operand, and how its lanes lie over the rows.
-template <int IO, int V, bool ADJACENT, int ROWS>
+template <int IO, int V, bool ADJACENT, int ROWS, bool MULTI>
 struct Place {
   bool second;
   int heads, steps;
-  uint32_t first, waves;   // the wave's first token, the operand's waves
-  int j, rg, rpw;
+  int at_once;             // tokens side by side
+  uint32_t first, stride;  // the wave's first token; from there to its next
+  int tau;                 // the lane's token of those
+  int j, rg, rpw;          // the lane of the row, the row of rpw heads at once
   bool in_row;
   int at;                  // the lane's first element; a lane without a piece reads the row's first
   bool turned;             // its elements are rotated
@@ -122,12 +154,20 @@ struct Place {
     second = (int)blockIdx.x >= a.split;
     const uint32_t wg = blockIdx.x - (second ? a.split : 0);
     const uint32_t wgs = second ? gridDim.x - a.split : a.split;
-    first = wg * kQkWaves + wave_id();
-    waves = wgs * kQkWaves;
     heads = second ? a.H[1] : a.H[0];
     j = lane_id() & (a.row.group - 1);
     rg = lane_id() / a.row.group;
     rpw = 64 / a.row.group;
+    at_once = 1;
+    tau = 0;
+    if constexpr (MULTI) {
+      at_once = second ? a.at_once[1] : a.at_once[0];
+      tau = rg & (at_once - 1);
+      rg /= at_once;
+      rpw /= at_once;
+    }
+    first = (wg * kQkWaves + wave_id()) * at_once;
+    stride = wgs * kQkWaves * at_once;
     steps = (heads + ROWS * rpw - 1) / (ROWS * rpw);
     in_row = j < a.row.lanes;
     at = in_row ? j * V : 0;
@@ -147,8 +187,14 @@ struct Place {
     const int h = head(step, u) + rg;
     return h < heads ? h : heads - 1;
   }
-  __device__ __forceinline__ bool writes(int step, int u) const {
-    return in_row && head(step, u) + rg < heads;
+  __device__ __forceinline__ bool writes(const Cursor& c, int u) const {
+    return in_row && c.there && head(c.step, u) + rg < heads;
+  }
+  __device__ __forceinline__ void start(const QkArgs& a, Cursor* c) const {
+    set_token<MULTI>(a, c, first, tau);
+  }
+  __device__ __forceinline__ void advance(const QkArgs& a, Cursor* c) const {
+    if (++c->step == steps) set_token<MULTI>(a, c, c->tok0 + stride, tau);
   }
   // element e's weight and its partner's (1 without)
   __device__ __forceinline__ void weights(const QkArgs& a, float* w, float* wp) const {
@@ -168,7 +214,8 @@ struct Place {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const bool later = ADJACENT ? e & 1 : at >= a.pairs;
-      const f32x2 t = *reinterpret_cast<const f32x2*>(trig + 2 * (pair + (ADJACENT ? e / 2 : e)));
+      const f32x2 t = *reinterpret_cast<const f32x2*>(
+          trig + 2 * (tau * a.pairs + pair + (ADJACENT ? e / 2 : e)));
       c[e] = turned ? t[0] : 1.f;
       s[e] = (SIGN > 0) == later ? t[1] : -t[1];
     }
@@ -198,11 +245,11 @@ template <int N> struct Count { static constexpr int value = N; };
 template <int IO, int V, bool PACKED> struct Source { typedef IoRow<IO, V> row; };
 template <int IO, int V> struct Source<IO, V, true> { typedef E4m3Row<V> row; };
 
-template <int IO, int V, bool PACKED, bool ADJACENT>
+template <int IO, int V, bool PACKED, bool ADJACENT, bool MULTI>
 __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(QkArgs a) {
-  __shared__ __align__(16) float trig_all[kQkWaves][2 * kMaxPairs];
+  __shared__ __align__(16) float trig_all[kQkWaves][2 * Turns<V, MULTI>::kPairs];
   constexpr int ES = Io<IO>::bytes;
-  const Place<IO, V, ADJACENT, kRows> pl(a);
+  const Place<IO, V, ADJACENT, kRows, MULTI> pl(a);
   const int D = a.row.D;
   const uint32_t tokens = (uint32_t)a.B * a.L;
   const RowView x = pl.second ? a.x[1] : a.x[0];
@@ -221,15 +268,15 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
   typename Source<IO, V, PACKED>::row ahead[kAhead][kRows];
   int scale[kAhead][kRows];
   Cursor ld, cur;
-  Turns turns;
-  set_token(a, &ld, pl.first);
+  Turns<V, MULTI> turns;
+  pl.start(a, &ld);
   cur = ld;
   if (a.pairs) {
-    turns_init(a, &turns);
-    turns_fetch(a, &turns, ld.tok);
+    turns.init(a, pl.at_once);
+    turns.fetch(a, ld.tok0);
   }
   auto load = [&](int i) {
-    if (ld.tok < tokens && ld.live) {
+    if (ld.tok0 < tokens && ld.live) {
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         const uint32_t h = pl.head_of(ld.step, u);
@@ -244,7 +291,7 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
         }
       }
     }
-    advance(a, &ld, pl.steps, pl.waves);
+    pl.advance(a, &ld);
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(i);
@@ -254,13 +301,14 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
     constexpr int N = decltype(count)::value;
     const int64_t row = (int64_t)cur.tok * pl.heads;
     IoRow<IO, V> out[N];
-    if (cur.live) {
+    if (MULTI || cur.live) {
       IoRow<IO, V> in[N];
       float f[N][V], inv[N];
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         if constexpr (PACKED) ahead[i][u].get(&in[u], scale[i][u]);
         else in[u] = ahead[i][u];
+        if constexpr (MULTI) in[u].keep(cur.live);   // rows of zeros behind the end (not read)
         in[u].get(f[u]);
         inv[u] = 1.f;
       }
@@ -274,7 +322,7 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
           const int sb = scale_byte(top[u]);
           E4m3Row<V> v;
           v.set(in[u], sb);
-          if (pl.writes(cur.step, u)) {
+          if (pl.writes(cur, u)) {
             const uint32_t h = pl.head(cur.step, u) + pl.rg;
             v.store(v8_out + row * D, h * D + pl.at);
             if (pl.j == 0) (s8_out + row)[h] = (uint8_t)sb;
@@ -312,7 +360,7 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         out[u].u = typename IoRow<IO, V>::words(0u);
-        if (!PACKED && v8_out && pl.writes(cur.step, u)) {
+        if (!PACKED && v8_out && pl.writes(cur, u)) {
           const uint32_t h = pl.head(cur.step, u) + pl.rg;
           E4m3Row<V> v;
           v.set(out[u], 0);
@@ -323,37 +371,37 @@ __global__ __launch_bounds__(kQkThreads, kWavesPerSimd) void qk_forward_kernel(Q
     }
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      if (pl.writes(cur.step, u))
+      if (pl.writes(cur, u))
         out[u].store(y + row * D * ES, ((pl.head(cur.step, u) + pl.rg) * D + pl.at) * ES);
   };
 
-  while (cur.tok < tokens) {
+  while (cur.tok0 < tokens) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (cur.tok >= tokens) break;
+      if (cur.tok0 >= tokens) break;
       if (cur.step == 0 && a.pairs) {
-        if (cur.live) {
-          token_turns(a, turns, trig);
+        if (MULTI || cur.live) {
+          turns.form(a, trig);
           pl.template coefficients<1>(a, trig, c, s);
 #pragma unroll
           for (int e = 0; e < V; ++e) c[e] *= w[e], s[e] *= wp[e];
         }
-        turns_fetch(a, &turns, cur.tok + pl.waves);
+        turns.fetch(a, cur.tok0 + pl.stride);
       }
       if (pl.both(cur.step)) process(Count<kRows>(), i);
       else process(Count<1>(), i);
       load(i);
-      advance(a, &cur, pl.steps, pl.waves);
+      pl.advance(a, &cur);
     }
   }
 }
 
-template <int IO, int V, bool PACKED, bool ADJACENT>
-__global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_kernel(QkArgs a) {
-  __shared__ __align__(16) float trig_all[kQkWaves][2 * kMaxPairs];
+template <int IO, int V, bool PACKED, bool ADJACENT, bool MULTI>
+__global__ __launch_bounds__(kQkThreads, back_waves_per_simd(MULTI)) void qk_backward_kernel(QkArgs a) {
+  __shared__ __align__(16) float trig_all[kQkWaves][2 * Turns<V, MULTI>::kPairs];
   __shared__ float sum[kRowMaxD];
   constexpr int ES = Io<IO>::bytes;
-  const Place<IO, V, ADJACENT, kBackRows> pl(a);
+  const Place<IO, V, ADJACENT, kBackRows, MULTI> pl(a);
   const int D = a.row.D;
   const uint32_t tokens = (uint32_t)a.B * a.L;
   const RowView x = pl.second ? a.x[1] : a.x[0], dx = pl.second ? a.dx[1] : a.dx[0];
@@ -370,15 +418,15 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
   IoRow<IO, V> gs[kBackAhead][kBackRows];
   int scale[kBackAhead][kBackRows];
   Cursor ld, cur;
-  Turns turns;
-  set_token(a, &ld, pl.first);
+  Turns<V, MULTI> turns;
+  pl.start(a, &ld);
   cur = ld;
   if (a.pairs) {
-    turns_init(a, &turns);
-    turns_fetch(a, &turns, ld.tok);
+    turns.init(a, pl.at_once);
+    turns.fetch(a, ld.tok0);
   }
   auto load = [&](int i) {
-    if (ld.tok < tokens && ld.live) {
+    if (ld.tok0 < tokens && ld.live) {
 #pragma unroll
       for (int u = 0; u < kBackRows; ++u) {
         const uint32_t h = pl.head_of(ld.step, u);
@@ -396,7 +444,7 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
         }
       }
     }
-    advance(a, &ld, pl.steps, pl.waves);
+    pl.advance(a, &ld);
   };
 #pragma unroll
   for (int i = 0; i < kBackAhead; ++i) load(i);
@@ -404,10 +452,11 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
   auto process = [&](auto count, int i) {
     constexpr int N = decltype(count)::value;
     IoRow<IO, V> out[N];
-    if (cur.live) {
+    if (MULTI || cur.live) {
       float g[N][V];
 #pragma unroll
       for (int u = 0; u < N; ++u) {
+        if constexpr (MULTI) gs[i][u].keep(cur.live);   // rows of zeros behind the end
         gs[i][u].get(g[u]);
         if (a.pairs) {
           float h[V];
@@ -420,6 +469,10 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
         float f[N][V], ss[N], dot[N], inv[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
+          if constexpr (MULTI) {
+            xs[i][u].keep(cur.live);
+            scale[i][u] = cur.live ? scale[i][u] : 127;
+          }
           if constexpr (PACKED) xs[i][u].get(f[u], scale[i][u]);
           else xs[i][u].get(f[u]);
           ss[u] = 0.f;
@@ -432,7 +485,7 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
         for (int u = 0; u < N; ++u) {
           inv[u] = row_inverse(fmaf(ss[u], a.c, a.eps));
           // lanes without a row of their own add nothing to dw, nor to the dot
-          const float own = pl.writes(cur.step, u) ? inv[u] : 0.f;
+          const float own = pl.writes(cur, u) ? inv[u] : 0.f;
           dot[u] = 0.f;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
@@ -461,25 +514,25 @@ __global__ __launch_bounds__(kQkThreads, kBackWavesPerSimd) void qk_backward_ker
               ((int64_t)cur.b * dx.sb + (int64_t)cur.l * dx.sl) * ES;
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      if (pl.writes(cur.step, u))
+      if (pl.writes(cur, u))
         out[u].store(p, ((pl.head(cur.step, u) + pl.rg) * D + pl.at) * ES);
   };
 
-  while (cur.tok < tokens) {
+  while (cur.tok0 < tokens) {
 #pragma unroll
     for (int i = 0; i < kBackAhead; ++i) {
-      if (cur.tok >= tokens) break;
+      if (cur.tok0 >= tokens) break;
       if (cur.step == 0 && a.pairs) {
-        if (cur.live) {
-          token_turns(a, turns, trig);
+        if (MULTI || cur.live) {
+          turns.form(a, trig);
           pl.template coefficients<-1>(a, trig, c, s);
         }
-        turns_fetch(a, &turns, cur.tok + pl.waves);
+        turns.fetch(a, cur.tok0 + pl.stride);
       }
       if (pl.both(cur.step)) process(Count<kBackRows>(), i);
       else process(Count<1>(), i);
       load(i);
-      advance(a, &cur, pl.steps, pl.waves);
+      pl.advance(a, &cur);
     }
   }
   if (!a.part) return;
@@ -520,92 +573,126 @@ __global__ __launch_bounds__(1024) void qk_weights_kernel(QkArgs a, int wgs) {
   if (slice == 0 && col < D) (blockIdx.y ? a.dw[1] : a.dw[0])[col] = sum[0][threadIdx.x & 31];
 }
 
-// Workgroups on each operand: one wave a token where there are no more than
-// `most`, else shared out by the steps of a token's rows.
-struct Shares {
-  int first, all;
-};
-static Shares shares(const QkArgs& a, int most) {
-  const int64_t need = ((int64_t)a.B * a.L + kQkWaves - 1) / kQkWaves;
-  if (2 * need <= most) return Shares{(int)need, (int)(2 * need)};
+// Tokens that a wave takes side by side for an operand of `heads` heads: the
+// most, a power of two, that leave room for all the heads in one step.  One of
+// 8 heads of 128 in bf16 fills a step by itself; of one head, 4 tokens.
+static int tokens_at_once(const QkArgs& a, int heads, int rows) {
   const int rpw = 64 / a.row.group;
-  const int64_t s0 = (a.H[0] + rpw - 1) / rpw, s1 = (a.H[1] + rpw - 1) / rpw;   // rows
-  int64_t n = (most * s0 + (s0 + s1) / 2) / (s0 + s1);
+  int n = 1;
+  while (2 * n <= rpw && rpw / (2 * n) * rows >= heads) n *= 2;
+  return n;
+}
+
+// Workgroups on each operand: one wave for each of its tokens (or of so many
+// side by side) where there are no more than `most`, else shared out by the
+// steps that a token's rows take.
+static int shares(QkArgs* a, int most, int rows) {
+  const int64_t tokens = (int64_t)a->B * a->L;
+  int64_t need[2];
+  double cost[2];
+  for (int i = 0; i < 2; ++i) {
+    const int n = a->at_once[i];
+    need[i] = (tokens + (int64_t)n * kQkWaves - 1) / ((int64_t)n * kQkWaves);
+    const int at = 64 / a->row.group / n * rows;
+    cost[i] = (double)((a->H[i] + at - 1) / at) / n;
+  }
+  if (need[0] + need[1] <= most) {
+    a->split = (int)need[0];
+    return (int)(need[0] + need[1]);
+  }
+  int64_t n = (int64_t)(most * cost[0] / (cost[0] + cost[1]) + 0.5);
   n = n < 1 ? 1 : n > most - 1 ? most - 1 : n;
-  const int64_t k = most - n < need ? most - n : need;
-  n = n < need ? n : need;
-  return Shares{(int)n, (int)(n + k)};
+  const int64_t k = most - n < need[1] ? most - n : need[1];
+  n = n < need[0] ? n : need[0];
+  a->split = (int)n;
+  return (int)(n + k);
 }
 
 int64_t qk_backward_parts(int64_t tokens) {
   const int64_t need = (tokens + kQkWaves - 1) / kQkWaves;
-  return 2 * need < kQkBackWgs ? 2 * need : kQkBackWgs;
+  return 2 * need < back_wgs(false) ? 2 * need : back_wgs(false);
 }
 
-template <bool PACKED, bool ADJACENT>
+template <bool PACKED, bool ADJACENT, bool MULTI>
 static void forward_as(const QkArgs& a, int io, int wgs, hipStream_t s) {
   const dim3 g(wgs), t(kQkThreads);
   if (io == IO_BF16) {
     if (a.row.V == 8)
-      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 8, PACKED, ADJACENT>), g, t, 0, s, a);
+      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 8, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
     else if (a.row.V == 4)
-      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 4, PACKED, ADJACENT>), g, t, 0, s, a);
+      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 4, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
     else
-      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 2, PACKED, ADJACENT>), g, t, 0, s, a);
+      hipLaunchKernelGGL((qk_forward_kernel<IO_BF16, 2, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
   } else {
     if (a.row.V == 4)
-      hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 4, PACKED, ADJACENT>), g, t, 0, s, a);
+      hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 4, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
     else
-      hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 2, PACKED, ADJACENT>), g, t, 0, s, a);
+      hipLaunchKernelGGL((qk_forward_kernel<IO_F32, 2, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
+  }
+}
+
+template <bool PACKED, bool ADJACENT, bool MULTI>
+static void backward_as(const QkArgs& a, int io, int wgs, hipStream_t s) {
+  const dim3 g(wgs), t(kQkThreads);
+  if (io == IO_BF16) {
+    if (a.row.V == 8)
+      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 8, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
+    else if (a.row.V == 4)
+      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 4, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
+    else
+      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 2, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
+  } else {
+    if (a.row.V == 4)
+      hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 4, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
+    else
+      hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 2, PACKED, ADJACENT, MULTI>), g, t, 0, s, a);
+  }
+}
+
+// Whether an operand's tokens go several at once.
+static bool side_by_side(QkArgs* a, int rows) {
+  for (int i = 0; i < 2; ++i) a->at_once[i] = tokens_at_once(*a, a->H[i], rows);
+  return a->at_once[0] > 1 || a->at_once[1] > 1;
+}
+
+template <bool BACK, bool PACKED, bool ADJACENT>
+static void tokens_as(const QkArgs& a, int io, bool multi, int wgs, hipStream_t s) {
+  if constexpr (BACK) {
+    if (multi) backward_as<PACKED, ADJACENT, true>(a, io, wgs, s);
+    else backward_as<PACKED, ADJACENT, false>(a, io, wgs, s);
+  } else {
+    if (multi) forward_as<PACKED, ADJACENT, true>(a, io, wgs, s);
+    else forward_as<PACKED, ADJACENT, false>(a, io, wgs, s);
+  }
+}
+
+template <bool BACK>
+static void launch_as(const QkArgs& a, int io, bool packed, bool multi, int wgs, hipStream_t s) {
+  if (packed) {
+    if (a.adjacent) tokens_as<BACK, true, true>(a, io, multi, wgs, s);
+    else tokens_as<BACK, true, false>(a, io, multi, wgs, s);
+  } else {
+    if (a.adjacent) tokens_as<BACK, false, true>(a, io, multi, wgs, s);
+    else tokens_as<BACK, false, false>(a, io, multi, wgs, s);
   }
 }
 
 hipError_t launch_qk_forward(const QkArgs& args, int io, bool packed, hipStream_t s) {
   QkArgs a = args;
-  const Shares sh = shares(a, kQkWgs);
-  a.split = sh.first;
-  if (packed) {
-    if (a.adjacent) forward_as<true, true>(a, io, sh.all, s);
-    else forward_as<true, false>(a, io, sh.all, s);
-  } else {
-    if (a.adjacent) forward_as<false, true>(a, io, sh.all, s);
-    else forward_as<false, false>(a, io, sh.all, s);
-  }
+  const bool multi = side_by_side(&a, kRows);
+  const int wgs = shares(&a, kQkWgs, kRows);
+  launch_as<false>(a, io, packed, multi, wgs, s);
   return hipGetLastError();
-}
-
-template <bool PACKED, bool ADJACENT>
-static void backward_as(const QkArgs& a, int io, int wgs, hipStream_t s) {
-  const dim3 g(wgs), t(kQkThreads);
-  if (io == IO_BF16) {
-    if (a.row.V == 8)
-      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 8, PACKED, ADJACENT>), g, t, 0, s, a);
-    else if (a.row.V == 4)
-      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 4, PACKED, ADJACENT>), g, t, 0, s, a);
-    else
-      hipLaunchKernelGGL((qk_backward_kernel<IO_BF16, 2, PACKED, ADJACENT>), g, t, 0, s, a);
-  } else {
-    if (a.row.V == 4)
-      hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 4, PACKED, ADJACENT>), g, t, 0, s, a);
-    else
-      hipLaunchKernelGGL((qk_backward_kernel<IO_F32, 2, PACKED, ADJACENT>), g, t, 0, s, a);
-  }
 }
 
 hipError_t launch_qk_backward(const QkArgs& args, int io, bool packed, hipStream_t s) {
   QkArgs a = args;
-  const Shares sh = shares(a, kQkBackWgs);
-  a.split = sh.first;
-  if (packed) {
-    if (a.adjacent) backward_as<true, true>(a, io, sh.all, s);
-    else backward_as<true, false>(a, io, sh.all, s);
-  } else {
-    if (a.adjacent) backward_as<false, true>(a, io, sh.all, s);
-    else backward_as<false, false>(a, io, sh.all, s);
-  }
+  const bool multi = side_by_side(&a, kBackRows);
+  const int wgs = shares(&a, back_wgs(multi), kBackRows);
+  launch_as<true>(a, io, packed, multi, wgs, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  hipLaunchKernelGGL(qk_weights_kernel, dim3((a.row.D + 31) / 32, 2), dim3(1024), 0, s, a, sh.all);
+  hipLaunchKernelGGL(qk_weights_kernel, dim3((a.row.D + 31) / 32, 2), dim3(1024), 0, s, a, wgs);
   return hipGetLastError();
 }
 

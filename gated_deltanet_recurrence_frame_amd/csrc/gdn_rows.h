@@ -28,6 +28,11 @@ struct IoRow {
   __device__ __forceinline__ void store(char* row, uint32_t off) const {
     *reinterpret_cast<words*>(row + off) = u;
   }
+  // zeros unless `yes`
+  __device__ __forceinline__ void keep(bool yes) {
+#pragma unroll
+    for (int e = 0; e < kWords; ++e) u[e] = yes ? u[e] : 0u;
+  }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
     for (int e = 0; e < kWords; ++e) {
@@ -77,6 +82,10 @@ struct E4m3Row {
     if constexpr (V == 8) *reinterpret_cast<u32x2*>(p) = u32x2{u[0], u[1]};
     else if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = u[0];
     else *reinterpret_cast<uint16_t*>(p) = (uint16_t)u[0];
+  }
+  __device__ __forceinline__ void keep(bool yes) {
+#pragma unroll
+    for (int e = 0; e < kWords; ++e) u[e] = yes ? u[e] : 0u;
   }
   // the values, times 2^(byte - 127)
   __device__ __forceinline__ void get(float* f, int byte) const {
