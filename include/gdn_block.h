@@ -27,8 +27,12 @@
  *     and pack8 are even.  Heads D > 128 need four elements' alignment in
  *     place of two (pointers, strides and a rotation's number of pairs), else
  *     GDN_ERR_MISALIGNED.  Rows that are 16-byte aligned are the fast case.
- *   - Sizes are at least 1; B * L at most 2^31 - 1, at most 2^40 elements a
- *     tensor, strides at most 2^40.
+ *   - Sizes are at least 1; B * L (qk, pack8: times the heads) at most
+ *     2^31 - 1, at most 2^40 elements a tensor, strides at most 2^40; lrec
+ *     also B * ceil(L / 128) * ceil(C / 64) below 2^23 (workgroups of a
+ *     launch).  Beyond: GDN_ERR_BAD_SHAPE.
+ *   - A workspace and a saved buffer belong to one call at a time: calls that
+ *     may overlap (other streams, two captured graphs) need their own.
  *   - `lengths` is NULL or B device int32s, the number of tokens of each
  *     sequence of a padded batch (values outside 0 .. L count as 0 or L).
  *     What the inputs hold behind a sequence's last token is never read; the
