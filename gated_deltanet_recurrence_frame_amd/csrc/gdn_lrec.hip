@@ -150,7 +150,7 @@ __device__ __forceinline__ uint32_t publishable(float f) {
 // What the workgroup's waves share of the state entering its chunk.
 template <int VEC, int WAVES>
 struct Entering {
-  Maps<VEC, WAVES> before;   // maps of the group's earlier chunks
+  Maps<VEC, WAVES> before;   // maps of the group's earlier chunks (several chunks only)
   float start[64 * VEC];     // the state entering the group
 };
 
@@ -178,7 +178,7 @@ __device__ __forceinline__ void entering_state(const LrecArgs& p, const Tile& t,
   const int w = wave_id(), col = lane_id() * VEC;
   const int64_t BC = (int64_t)p.B * p.C, bc = (int64_t)t.b * p.C + t.c0 + t.cl;
   const int g = t.step / kGroup, r = t.step % kGroup;
-  const bool several = WAVES > 1 && p.chunks > 1;
+  const bool several = WAVES == kLrecWaves && p.chunks > 1;
   if (several) {
     if (w == 0 && t.in && r != kGroup - 1 && !t.last) {
 #pragma unroll
@@ -532,33 +532,52 @@ __global__ __launch_bounds__(256) void lrec_clear_kernel(u32x4* ws, int64_t n) {
   }
 }
 
+template <int N> struct Waves { static constexpr int value = N; };
+
 static void clear(const LrecArgs& p, hipStream_t s) {
   const int64_t n = p.ws_bytes / 16, wgs = (n + 255) / 256;
   hipLaunchKernelGGL(lrec_clear_kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, s,
                      reinterpret_cast<u32x4*>(p.ticket), n);
 }
 
+// Sequences of one chunk take as many waves a workgroup as their tokens
+// fill (1, 2, 4 or all): a workgroup holds its registers until its last wave
+// ends.  In bf16 at 2240 channels, 1024 sequences of 17 tokens take 126 us in
+// workgroups of 8 waves and 44 in ones of 2; 16 sequences of one token 9.4 us
+// in 8 waves and 4.1 in one.
+template <typename LAUNCH>
+static void with_waves(const LrecArgs& p, LAUNCH launch) {
+  if (p.L <= kTokens) launch(Waves<1>());
+  else if (p.L <= 2 * kTokens) launch(Waves<2>());
+  else if (p.L <= 4 * kTokens) launch(Waves<4>());
+  else launch(Waves<kLrecWaves>());
+}
+
 template <int IO, int VEC, bool LOGITS>
 static hipError_t forward_as(const LrecArgs& p, bool states, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(64 * kLrecWaves);
+  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips));
   if (p.chunks > 1) clear(p, s);
-  if (states)
-    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, kLrecWaves, LOGITS, true>), g, t, 0, s, p);
-  else if (p.L <= kTokens)
-    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, 1, LOGITS, false>), g, dim3(64), 0, s, p);
-  else
-    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, kLrecWaves, LOGITS, false>), g, t, 0, s, p);
+  if (states) {
+    hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, kLrecWaves, LOGITS, true>), g,
+                       dim3(64 * kLrecWaves), 0, s, p);
+  } else {
+    with_waves(p, [&](auto waves) {
+      constexpr int W = decltype(waves)::value;
+      hipLaunchKernelGGL((lrec_forward_kernel<IO, VEC, W, LOGITS, false>), g, dim3(64 * W), 0, s,
+                         p);
+    });
+  }
   return hipGetLastError();
 }
 
 template <int IO, int VEC, bool LOGITS>
 static hipError_t backward_as(const LrecArgs& p, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips)), t(64 * kLrecWaves);
+  const dim3 g((unsigned)((int64_t)p.chunks * p.B * p.strips));
   if (p.chunks > 1) clear(p, s);
-  if (p.L <= kTokens)
-    hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, 1, LOGITS>), g, dim3(64), 0, s, p);
-  else
-    hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, kLrecWaves, LOGITS>), g, t, 0, s, p);
+  with_waves(p, [&](auto waves) {
+    constexpr int W = decltype(waves)::value;
+    hipLaunchKernelGGL((lrec_backward_kernel<IO, VEC, W, LOGITS>), g, dim3(64 * W), 0, s, p);
+  });
   return hipGetLastError();
 }
 

@@ -71,7 +71,8 @@ def run(c, io, logits, complement, x=None, z=None):
     return o, h, g
 
 
-SHAPES = [(1, 1, 1), (3, 1, 8), (1, 2, 3), (2, 15, 5), (1, 16, 256), (1, 17, 260), (2, 127, 12),
+SHAPES = [(1, 1, 1), (3, 1, 8), (1, 2, 3), (2, 15, 5), (1, 16, 256), (1, 17, 260), (2, 32, 40),
+          (3, 33, 8), (2, 64, 36), (3, 65, 12), (2, 127, 12),
           (2, 128, 8), (1, 129, 64), (3, 300, 31), (1, 1000, 2), (2, 2177, 36), (1, 4500, 4)]
 
 
