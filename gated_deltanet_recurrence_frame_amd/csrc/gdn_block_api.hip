@@ -113,7 +113,10 @@ bool fits(int V, int B, int L, int D, int pairs, const RowUse* use, int n) {
   return true;
 }
 // The widest pieces that fit: 16 bytes of the io type where rows allow, else
-// 8 or 4 (bf16) or 8 (fp32); 0 if none do.
+// 8 or 4 (bf16) or 8 (fp32); 0 if none do.  In bf16 over 106,480 tokens of 20
+// heads of 112, pieces of 16, 8 and 4 bytes: qk forward 381, 436 and 733 us,
+// pack8 124, 130 and 218, unpack8 121, 132 and 162; in fp32 16 and 8 bytes: qk
+// forward 666 and 1086 us.
 RowShape row_shape(int B, int L, int D, int pairs, int io, const RowUse* use, int n) {
   RowShape r{D, 0, 0, 0};
   for (int V = io == IO_BF16 ? 8 : 4; V >= 2 && !r.V; V /= 2)
@@ -290,7 +293,8 @@ struct LrecUse {
   const int64_t* stride;
 };
 // The widest vector of at most `most` elements that the channels, strides and
-// pointers allow.
+// pointers allow.  Two bf16 a lane against one, 106,480 tokens of 2240
+// channels: forward (states saved) 338 us against 406, backward 476 against 573.
 int lrec_vec(const gdn_lrec_problem* p, int es, int most, const LrecUse* use, int n) {
   if (p->C % most) return 1;
   for (int i = 0; i < n; ++i) {

@@ -20,19 +20,34 @@
 // An operand of few heads leaves lanes without a row: a wave then takes
 // several tokens side by side (MULTI; as many, a power of two, as leave their
 // heads room in a step: tokens_at_once).
+//
+// Bytes bound both passes.  106,480 tokens of 20 + 20 heads of 112 in bf16,
+// rotated on three axes: forward 366 us (1.91 GB, 5.2 TB/s; a plain copy
+// reaches 5.05-5.3), with checkpoints written 485 us (2.39 GB, three fifths of
+// it written: reads at 6.17 and writes at 4.57 TB/s would take 469), backward
+// from checkpoints 485 us (2.39 GB).  The VALU is busy for half of that.  What
+// brought it there: rows loaded steps ahead of their use (748 -> 544 us
+// forward, 986 -> 591 backward), the scaling conversions and hardware turns
+// (VALU instructions 201 M -> 116 M), whole rows an access instead of two
+// half-row pieces a lane (531 -> 484 us).
 #include "gdn_rows.h"
 
 namespace gdn {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkWaves = kQkThreads / 64;
+// Two rows a lane in a step against one: forward 484 us against 492, backward
+// 486 against 511.  Two steps ahead are as good as three forward (485); the
+// backward's two operands a row fill its registers at one (486; spilled at
+// two, 516, and three, 708).
 constexpr int kRows = 2;            // rows of a lane in a step (forward)
 constexpr int kBackRows = 2;        // (backward)
 constexpr int kAhead = 2;           // steps loaded ahead (forward)
 constexpr int kBackAhead = 1;       // (backward)
 // Waves a SIMD that the registers are bounded for, and with them workgroups at
 // most: as many as the card holds at once (256 CUs, 4 SIMDs with one wave of a
-// workgroup each); one more would run alone at the end.
+// workgroup each).  A quarter more ran alone at the end (598 us against 531),
+// twice as many shorter ones are no faster (488 against 486).
 constexpr int kWavesPerSimd = 4;
 constexpr int back_waves_per_simd(bool multi) { return multi ? 3 : 4; }
 constexpr int kQkWgs = 256 * kWavesPerSimd;
@@ -575,7 +590,10 @@ __global__ __launch_bounds__(1024) void qk_weights_kernel(QkArgs a, int wgs) {
 
 // Tokens that a wave takes side by side for an operand of `heads` heads: the
 // most, a power of two, that leave room for all the heads in one step.  One of
-// 8 heads of 128 in bf16 fills a step by itself; of one head, 4 tokens.
+// 8 heads of 128 in bf16 fills a step by itself; of one head, 4 tokens.  Over
+// 106,480 tokens of 112, one token after the other against side by side, us
+// forward and backward: 1 + 1 heads 115 and 114 against 66 and 69, 8 + 1 heads
+// 172 and 197 against 156 and 166, 4 + 4 heads 129 and 155 against 134 and 139.
 static int tokens_at_once(const QkArgs& a, int heads, int rows) {
   const int rpw = 64 / a.row.group;
   int n = 1;
