@@ -14,6 +14,15 @@ namespace gdn {
 constexpr int kPackThreads = 256;
 constexpr int kPackWaves = kPackThreads / 64;
 constexpr int kPackRows = 4;    // rows of a lane in flight
+// A grid's threads along an axis end below 2^32; 2^31 rows can take 2^27
+// workgroups: so many lie along x, the rest along y.
+constexpr int kPackAcrossBits = 20;
+
+// The first of a lane's rows, the others `rpw` apart.
+__device__ __forceinline__ uint32_t first_row(int rpw, int rg) {
+  const uint32_t wg = (uint32_t)blockIdx.y << kPackAcrossBits | blockIdx.x;
+  return (wg * kPackWaves + wave_id()) * rpw * kPackRows + rg;
+}
 
 // Row r (of B L H) of the strided tensor.
 template <int IO>
@@ -32,7 +41,7 @@ __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackArgs a) {
   const uint32_t rows = (uint32_t)a.B * a.L * a.H;
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
   const bool in_row = j < a.row.lanes;
-  const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
+  const uint32_t base = first_row(rpw, rg);
   const uint32_t at = in_row ? j * V : 0;   // a lane without a piece reads the row's first
   IoRow<IO, V> x[kPackRows];
 #pragma unroll
@@ -63,7 +72,7 @@ __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
   const int rpw = 64 / a.row.group;
   const uint32_t rows = (uint32_t)a.B * a.L * a.H;
   const int lane = lane_id(), j = lane & (a.row.group - 1), rg = lane / a.row.group;
-  const uint32_t base = (blockIdx.x * kPackWaves + wave_id()) * rpw * kPackRows + rg;
+  const uint32_t base = first_row(rpw, rg);
   if (j >= a.row.lanes) return;
   const uint32_t at = j * V;
   E4m3Row<V> v[kPackRows];
@@ -86,14 +95,15 @@ __global__ __launch_bounds__(kPackThreads) void unpack8_kernel(PackArgs a) {
   }
 }
 
-static unsigned pack_grid(const PackArgs& a) {
+static dim3 pack_grid(const PackArgs& a) {
   const int64_t rows = (int64_t)a.B * a.L * a.H;
   const int64_t per = (int64_t)kPackWaves * (64 / a.row.group) * kPackRows;
-  return (unsigned)((rows + per - 1) / per);
+  const int64_t wgs = (rows + per - 1) / per, across = int64_t(1) << kPackAcrossBits;
+  return dim3((unsigned)(wgs < across ? wgs : across), (unsigned)((wgs + across - 1) / across));
 }
 
 hipError_t launch_pack8(const PackArgs& a, int io, hipStream_t s) {
-  const dim3 g(pack_grid(a)), t(kPackThreads);
+  const dim3 g = pack_grid(a), t(kPackThreads);
   if (io == IO_BF16) {
     if (a.row.V == 8) hipLaunchKernelGGL((pack8_kernel<IO_BF16, 8>), g, t, 0, s, a);
     else if (a.row.V == 4) hipLaunchKernelGGL((pack8_kernel<IO_BF16, 4>), g, t, 0, s, a);
@@ -106,7 +116,7 @@ hipError_t launch_pack8(const PackArgs& a, int io, hipStream_t s) {
 }
 
 hipError_t launch_unpack8(const PackArgs& a, int io, hipStream_t s) {
-  const dim3 g(pack_grid(a)), t(kPackThreads);
+  const dim3 g = pack_grid(a), t(kPackThreads);
   if (io == IO_BF16) {
     if (a.row.V == 8) hipLaunchKernelGGL((unpack8_kernel<IO_BF16, 8>), g, t, 0, s, a);
     else if (a.row.V == 4) hipLaunchKernelGGL((unpack8_kernel<IO_BF16, 4>), g, t, 0, s, a);

@@ -274,6 +274,23 @@ def test_pack8_strided_and_into_slices():
     assert bool((buf[:, :, :4] == 3.0).all()) and bool((buf[:, :, 8:] == 3.0).all())
 
 
+def test_pack8_of_more_workgroups_than_a_grid_axis_holds():
+    # 2^28 rows, 16 a workgroup, one token's repeated (pieces of two elements)
+    L, H, D = (1 << 24) + 3, 16, 68
+    one = rows(np.random.Generator(np.random.PCG64(16)), (H * D + 2,), "bf16").to(DEV)
+    x = one[2:].view(1, 1, H, D)
+    c = block.pack8(x.expand(1, L, H, D))
+    ref = block.pack8(x)
+    back = torch.empty(L * H * D + 2, dtype=torch.bfloat16, device=DEV)[2:].view(1, L, H, D)
+    block.unpack8(c, out=back)
+    want = block.unpack8(ref)
+    for t in range(0, L, 1 << 21):
+        part = slice(t, t + (1 << 21))
+        assert bool((c.values.view(torch.uint8)[:, part] == ref.values.view(torch.uint8)).all())
+        assert bool((c.scale[:, part] == ref.scale).all())
+        assert bool((back[:, part] == want).all())
+
+
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
 @pytest.mark.parametrize("pairing", ["halves", "adjacent"])
 @pytest.mark.parametrize("shape", [SHAPES[1], SHAPES[2], SHAPES[3], SHAPES[4]], ids=str)
