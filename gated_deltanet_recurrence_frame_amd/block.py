@@ -101,6 +101,8 @@ def _device(device):
 def _call(dev, f, name, *args):
     """The entry point f on `dev`'s current stream, with `dev` current."""
     i = dev.index
+    if i is None:
+        raise ValueError("%s runs on a GPU, the tensors are on %s" % (name, dev))
     if torch.cuda.current_device() != i:
         with torch.cuda.device(dev):
             _check(f(*args, torch._C._cuda_getCurrentRawStream(i)), name)
@@ -182,15 +184,17 @@ def pack8(x, out=None):
     return out
 
 
-def unpack8(checkpoint, dtype=torch.bfloat16, out=None):
-    """Rows [B, L, H, D] of a checkpoint, in bf16 or fp32 (gdn_unpack8)."""
+def unpack8(checkpoint, dtype=None, out=None):
+    """Rows [B, L, H, D] of a checkpoint, in bf16 (also None) or fp32
+    (gdn_unpack8), or those of `out`."""
     v = checkpoint.values
     if v.dim() != 4:
         raise ValueError("checkpoint values must be [B, L, H, D]")
     shape, dev = v.shape, v.device
     c = GdnCheckpoint(*_checkpoint(checkpoint, "checkpoint", shape, dev))
-    out = out if out is not None else _empty(shape, dtype, dev)
-    prob = _pack8_problem(shape, _io_of(out), _view(out, "out", dtype, shape, dev))
+    if out is None:
+        out = _empty(shape, dtype or torch.bfloat16, dev)
+    prob = _pack8_problem(shape, _io_of(out), _view(out, "out", dtype or out.dtype, shape, dev))
     _call(dev, lib().gdn_unpack8, "gdn_unpack8", ctypes.byref(prob), ctypes.byref(c),
           out.data_ptr())
     return out
@@ -259,11 +263,14 @@ class QkPlan:
         self.q_out = _empty(self.q_shape, self.dtype, self.device)
         self.k_out = _empty(self.k_shape, self.dtype, self.device)
 
-    def _backward_buffers(self):
+    def _backward_buffers(self, dq=None, dk=None):
+        """What the backward writes, but for the gradients that it is given."""
         dev = self.device
-        self.dq = _empty(self.q_shape, self.dtype, dev)
-        self.dk = _empty(self.k_shape, self.dtype, dev)
-        if self.weights:
+        if dq is None and self.dq is None:
+            self.dq = _empty(self.q_shape, self.dtype, dev)
+        if dk is None and self.dk is None:
+            self.dk = _empty(self.k_shape, self.dtype, dev)
+        if self.weights and self.dw is None:
             self.dw = _empty((2, self.D), torch.float32, dev)
             self.ws = _empty(max(16, qk_workspace_size(self.prob, True)), torch.uint8, dev)
 
@@ -334,8 +341,7 @@ class QkPlan:
         rest = self._rest(positions, q_weight, k_weight, lengths)
         d_qp = _flat(d_q, "d_q", self.dtype, self.q_shape, dev)
         d_kp = _flat(d_k, "d_k", self.dtype, self.k_shape, dev)
-        if (dq is None or dk is None or self.weights and self.dw is None) and self.dq is None:
-            self._backward_buffers()
+        self._backward_buffers(dq, dk)
         dq, dk = self.dq if dq is None else dq, self.dk if dk is None else dk
         dqs = _view(dq, "dq", self.dtype, self.q_shape, dev, self._inner)
         dks = _view(dk, "dk", self.dtype, self.k_shape, dev, self._inner)

@@ -18,7 +18,8 @@
  * gdn_status results, capture into HIP graphs), with these differences:
  *   - Inputs that a block takes out of one projection may be strided views:
  *     element (b, l, h, d) of q at q[b stride[0] + l stride[1] + h D + d],
- *     strides in elements.  Strides of inputs are >= 0 (0 repeats a row);
+ *     strides in elements.  Strides of inputs are >= 0 (0 repeats a row; its
+ *     gradient is written once for every place that reads it, not summed);
  *     rows of an output must not overlap each other.  Two outputs, or an
  *     output and an input, may be interleaved views of one allocation.
  *   - io pointers need the alignment of two elements for qk and pack8 (4
@@ -146,7 +147,10 @@ gdn_status gdn_qk_backward(const gdn_qk_problem* p, const void* q, const void* k
  *   a   = gate, or sigmoid(gate) with GDN_FLAG_GATE_LOGITS,
  *   u   = x, or (1 - a) x with GDN_LREC_COMPLEMENT.
  * A gate of exactly 0 (a logit of -inf) starts the state anew.  The state
- * and both scans are fp32; o is rounded once to the io type. */
+ * and both scans are fp32; o is rounded once to the io type.  The scans form
+ * products of the gates of up to 128 consecutive tokens: gates beyond 1 in
+ * magnitude (values; logits have none) must leave those finite, or the
+ * channel's state is NaN from there on. */
 enum { GDN_LREC_COMPLEMENT = 4 };   /* a bit beside gdn_flag's */
 
 typedef struct {

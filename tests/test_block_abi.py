@@ -380,3 +380,15 @@ def test_checkpoint_checks(lib):
         block.unpack8(block.Checkpoint(v.view(torch.float8_e4m3fn), s[:, 1:]))
     with pytest.raises(TypeError):
         block.unpack8(block.Checkpoint(v.view(torch.float8_e4m3fn), s), torch.float16)
+
+
+def test_tensors_off_the_gpu_are_refused(lib):
+    x = torch.zeros((1, 2, 3, 16), dtype=torch.bfloat16)
+    r, h = torch.zeros((2, 1, 8)), torch.zeros((2, 8))
+    c = block.Checkpoint(torch.zeros(x.shape, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                         torch.zeros((1, 2, 3), dtype=torch.uint8))
+    for f in (lambda: block.pack8(x), lambda: block.unpack8(c), lambda: block.qk_forward(x, x),
+              lambda: block.qk_backward(x, x, x, x), lambda: block.lrec_forward(r, r),
+              lambda: block.lrec_step(r, r, h), lambda: block.lrec_backward(r, r, r)):
+        with pytest.raises(ValueError, match="runs on a GPU"):
+            f()

@@ -274,6 +274,15 @@ def test_pack8_strided_and_into_slices():
     assert bool((buf[:, :, :4] == 3.0).all()) and bool((buf[:, :, 8:] == 3.0).all())
 
 
+def test_unpack8_takes_the_type_of_its_output():
+    x = rows(np.random.Generator(np.random.PCG64(15)), (1, 5, 2, 64), "fp32").to(DEV)
+    c = block.pack8(x)
+    out = torch.empty_like(x)
+    assert block.unpack8(c, out=out) is out
+    assert torch.equal(out, block.unpack8(c, torch.float32))
+    assert torch.equal(out.bfloat16(), block.unpack8(c))
+
+
 def test_pack8_of_more_workgroups_than_a_grid_axis_holds():
     # 2^28 rows, 16 a workgroup, one token's repeated (pieces of two elements)
     L, H, D = (1 << 24) + 3, 16, 68
@@ -372,3 +381,18 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_backward_into_given_gradients_makes_none_of_its_own():
+    shape = (1, 40, 3, 2, 64, (32,))
+    c = case(*shape, "bf16", seed=17)
+    q, k, pos, wq, wk, d0, d1 = (on(t) for t in (c["q"], c["k"], c["positions"], c["wq"], c["wk"],
+                                                 *c["dy"]))
+    plan = block.QkPlan(*shape[:5], "bf16", DEV, axis_pairs=shape[5], weights=True)
+    dq, dk = torch.empty_like(q), torch.empty_like(k)
+    g = plan.backward(d0, d1, q, k, pos, wq, wk, dq=dq, dk=dk)
+    assert g["dq"] is dq and g["dk"] is dk and plan.dq is None and plan.dk is None
+    got = [t.clone() for t in g.values()]
+    for a, b in zip(got, plan.backward(d0, d1, q, k, pos, wq, wk, dk=dk).values()):
+        assert torch.equal(a, b)
+    assert plan.dk is None and plan.dq is not None
